@@ -33,7 +33,8 @@
  *    frees or retains them past the call.
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
  *    stream). Kernels run on it; every call returns only after its results
- *    (transcript updates, proof bytes) are on the host.
+ *    (transcript updates, proof bytes) are on the host, but for those whose
+ *    results are device buffers and that say that they only queue kernels.
  *  - Scratch memory comes from a per-context device arena that grows on
  *    demand (cudaMalloc) and is released by fp_ctx_destroy.
  *  - Return value: FP_OK (0), a positive warning, or a negative FP_ERR_*
@@ -743,6 +744,94 @@ int logup_prove_exp(fp_ctx* ctx, fp_tx* tx, const int16_t* g, const int16_t* s, 
 
 /* The numerator table's 2^16 entries exp_q(v), v = -2^15 .. 2^15 - 1, into host out (no GPU work). */
 int fp_exp_table(int32_t* out);
+
+/*
+ * Operators of the layer around the proven products. The statements above take int8 activations,
+ * the experts' inputs and integer outputs as given; these make the int8 activations from real ones,
+ * compute the products with real scales that a serving program answers with, and move tokens to
+ * their experts and back ("How fast can FlashProve go", 2 Background, the note on MoE layers).
+ *
+ * All of them: device pointers on the context's device, every buffer the caller's, nothing
+ * allocated. The kernels are queued on `stream` and the call returns without waiting, so that calls
+ * may be captured into a CUDA graph; buffers stay alive and unchanged until the stream has passed
+ * the call. The caller's current device is left as it was. Calls on different streams, and graphs
+ * that hold them, share no memory of the library's. Pitches are in elements (bytes where said) from
+ * row to row, not below the row's length; a single row's is not looked at. Inputs may not overlap
+ * outputs unless said. Errors: FP_ERR_ARG (null or misaligned pointer, bad type), FP_ERR_SHAPE,
+ * FP_ERR_CUDA.
+ */
+enum { FP_F32 = 0, FP_F16 = 1, FP_BF16 = 2 }; /* types of real values */
+
+/*
+ * Activations to int8 with one scale a token: a_t = max_j |x[t][j]|, scale = a_t / 127 (fp32),
+ * q = the integer nearest to 127 x[t][j] / a_t, ties to the even one (exactly, whatever the type).
+ * A row of zeros has scale 0; a row with a NaN or an infinity has integers 0 and a NaN scale. The
+ * result is what fp_matmul_i8 and an fp_site's xt take.
+ *  x      T rows of K values of x_type, pitch ldx.
+ *  pos    nullable. Null: token t's row is row t of q and scale (R >= T). Else T x k int32: token t
+ *         is written to rows pos[t][j] for every j < k; positions outside [0, R) are passed over.
+ *  q      R rows of K, pitch ldq. scale: R. Rows that no token goes to are left as they were.
+ * 0 <= T <= 2^24, 1 <= K <= 2^20, 0 <= R < 2^31, T k < 2^31.
+ */
+int fp_quantize_rows(fp_ctx* ctx, const void* x, int x_type, int64_t T, int64_t K, int64_t ldx, const int32_t* pos,
+                     int k, int64_t R, int8_t* q, int64_t ldq, float* scale, void* stream);
+
+/*
+ * Matrix product in 8-bit integers with a scale for each token and each output channel, dense or
+ * grouped by expert: y[n][m] = x_scale[n] w_scale[e][m] sum_k w[e][m][k] x[n][k]. The sum is exact;
+ * it is multiplied by the token's scale, then the channel's, in fp32 and rounded to y_type.
+ *  w        E x M rows of K int8, pitch ldw; w_scale: E x M.
+ *  x        N rows of K int8, pitch ldx; x_scale: N.
+ *  offsets  nullable when E = 1. E + 1 int32 as fp_moe_sort writes them: expert e has the rows
+ *           offsets[e] .. offsets[e + 1] - 1. Rows of y that no expert has are left as they were.
+ *           Offsets outside [0, N] or falling are clamped, so that nothing is read or written out
+ *           of bounds.
+ *  y        N rows of M values of y_type, pitch ldy.
+ * 1 <= M <= 2^24, 0 <= N <= 2^24, 1 <= K < 2^17 (exact int32 sums), 1 <= E <= 4096, E M < 2^31 - 255.
+ * Fastest when w, x, ldw and ldx are multiples of 16.
+ */
+int fp_matmul_i8(fp_ctx* ctx, const int8_t* w, int64_t ldw, const float* w_scale, int E, int64_t M, int64_t K,
+                 const int8_t* x, int64_t ldx, const float* x_scale, int64_t N, const int32_t* offsets, void* y,
+                 int y_type, int64_t ldy, void* stream);
+
+/*
+ * Tokens sorted by expert. e: n = T k int32, the experts of choices i = t k + j; an expert outside
+ * [0, E) is none (a token of padding). offsets: E + 1 int32, offsets[x] = #{i : 0 <= e_i < x}. pos: n
+ * int32, the row of every choice: offsets[e_i] + #{i' < i : e_i' = e_i}, -1 for none. With k = 1 this
+ * is the order of sumcheck_prove_dispatch. 0 <= n < 2^31, 1 <= E <= 4096.
+ */
+int fp_moe_sort(fp_ctx* ctx, const int32_t* e, int64_t n, int E, int32_t* offsets, int32_t* pos, void* stream);
+
+/*
+ * Rows to their experts: rows[pos[t][j]] = x[t] for every j < k; positions outside [0, R) are passed
+ * over and rows that no token goes to are left as they were. Rows are bytes of any type: row_bytes of
+ * them, pitches ldx and ldr in bytes. Its gradient is fp_moe_combine without weights.
+ * 0 <= T <= 2^24, T k < 2^31, 0 <= R < 2^31, 1 <= row_bytes <= 2^24.
+ */
+int fp_moe_dispatch(fp_ctx* ctx, const void* x, int64_t T, int64_t row_bytes, int64_t ldx, const int32_t* pos, int k,
+                    int64_t R, void* rows, int64_t ldr, void* stream);
+
+/*
+ * The experts' rows back to their tokens: out[t] = base[t] + sum_j weights[t][j] rows[pos[t][j]], summed
+ * in fp32 in the order of j and rounded once; positions outside [0, R) add nothing.
+ *  weights  nullable (all 1): T x k fp32.   base  nullable (0): T rows of M of out_type, pitch ldb, for
+ *           instance a shared expert's output; base may be out.
+ * 0 <= T <= 2^24, T k < 2^31, 0 <= R < 2^31, 1 <= M <= 2^24.
+ */
+int fp_moe_combine(fp_ctx* ctx, const void* rows, int rows_type, int64_t R, int64_t ldr, const int32_t* pos,
+                   const float* weights, const void* base, int64_t ldb, int64_t T, int k, int64_t M, void* out,
+                   int out_type, int64_t ldo, void* stream);
+
+/*
+ * Gradients of fp_moe_combine from dout (T rows of M of out_type, pitch ldd; also the gradient of
+ * base): drows[pos[t][j]] = weights[t][j] dout[t] and dweights[t][j] = sum_m dout[t][m]
+ * rows[pos[t][j]][m], fp32 sums in a fixed order; positions outside [0, R) have dweights 0. Rows of
+ * drows that no choice has are left as they were. drows (R rows of M of rows_type, pitch lddr) or
+ * dweights (T x k fp32) may be null; rows is not read without dweights. Sizes as fp_moe_combine.
+ */
+int fp_moe_combine_grad(fp_ctx* ctx, const void* dout, int out_type, int64_t ldd, const void* rows, int rows_type,
+                        int64_t R, int64_t ldr, const int32_t* pos, const float* weights, int64_t T, int k, int64_t M,
+                        void* drows, int64_t lddr, float* dweights, void* stream);
 
 /*
  * Self-test of the bounded device waits. The sum-check kernels stay resident

@@ -112,6 +112,13 @@ def lib():
     L.logup_prove_rescale_hi.argtypes = [vp, vp, C.POINTER(_Site), i32, vp, C.POINTER(sz), vp]
     L.sumcheck_prove_dispatch.argtypes = [vp, vp, vp, vp, vp, C.c_int64, C.c_int64, i32, vp, C.POINTER(sz), vp]
     L.fp_lhr_protocol_drive.argtypes = [vp, i32, i32, vp, vp, _VALUES_FN, vp, vp, C.POINTER(sz)]
+    i64 = C.c_int64
+    L.fp_quantize_rows.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, i64, vp, i64, vp, vp]
+    L.fp_matmul_i8.argtypes = [vp, vp, i64, vp, i32, i64, i64, vp, i64, vp, i64, vp, vp, i32, i64, vp]
+    L.fp_moe_sort.argtypes = [vp, vp, i64, i32, vp, vp, vp]
+    L.fp_moe_dispatch.argtypes = [vp, vp, i64, i64, i64, vp, i32, i64, vp, i64, vp]
+    L.fp_moe_combine.argtypes = [vp, vp, i32, i64, i64, vp, vp, vp, i64, i64, i32, i64, vp, i32, i64, vp]
+    L.fp_moe_combine_grad.argtypes = [vp, vp, i32, i64, vp, i32, i64, i64, vp, vp, i64, i32, i64, vp, i64, vp, vp]
     L.fp_ctx_set_profiling.argtypes = [vp, i32]
     L.fp_session_selftest.argtypes = [vp, vp]
     L.fp_host_stats.argtypes = [vp, C.POINTER(C.c_double)]
@@ -615,6 +622,19 @@ def _stream(stream) -> Optional[int]:
     return int(getattr(stream, "cuda_stream", stream))
 
 
+_REAL = {"float32": 0, "float16": 1, "bfloat16": 2}  # FP_F32, FP_F16, FP_BF16
+
+
+def _dtype(t) -> str:
+    return str(t.dtype).rsplit(".", 1)[-1]
+
+
+def _real(what: str, name: str, t) -> int:
+    if _dtype(t) not in _REAL:
+        raise ValueError(f"{what}: {name} must be float32, float16 or bfloat16, not {_dtype(t)}")
+    return _REAL[_dtype(t)]
+
+
 class SiteDesc:
     """One product Y = W . X: device tensors (anything with data_ptr()) and sizes.
 
@@ -737,6 +757,7 @@ class Context:
 
     def __init__(self, device: int = 0):
         self._L = lib()
+        self.device = int(device)
         self.h = self._L.fp_ctx_create(device)
         if not self.h:
             raise FpError(-3, f"fp_ctx_create({device}) failed (no usable CUDA device?)")
@@ -981,6 +1002,128 @@ class Context:
         self._check(self._L.fp_ffn_hidden(self.h, _ptr(s8), _ptr(u), int(s8.numel()), kh, _ptr(q), _ptr(r),
                                           _ptr(y), _stream(stream)), "fp_ffn_hidden")
 
+    # -- operators of the layer around the proven products: kernels queued on the stream (the current
+    # one of the context's device), buffers the caller's --
+
+    def _op_stream(self, stream) -> Optional[int]:
+        if stream is None:
+            import torch
+            return int(torch.cuda.current_stream(self.device).cuda_stream)
+        return _stream(stream)
+
+    def _tensor(self, what: str, name: str, t, shape, dtype: Optional[str] = None, dense: bool = False):
+        """Check a device tensor's type, shape (None: any) and layout; returns its row pitch. Rows of a
+        two-dimensional tensor may be part of wider ones unless it has to be dense."""
+        if t.device.type != "cuda" or t.device.index != self.device:
+            raise ValueError(f"{what}: {name} must be on cuda:{self.device}, not {t.device}")
+        if dtype is not None and _dtype(t) != dtype:
+            raise ValueError(f"{what}: {name} must be {dtype}, not {_dtype(t)}")
+        if t.dim() != len(shape) or any(a is not None and int(a) != int(b) for a, b in zip(shape, t.shape)):
+            want = " x ".join("?" if a is None else str(int(a)) for a in shape)
+            raise ValueError(f"{what}: {name} must be {want}, not {' x '.join(map(str, t.shape))}")
+        if dense or t.dim() != 2:
+            if not t.is_contiguous():
+                raise ValueError(f"{what}: {name} must be contiguous")
+            return int(t.shape[-1])
+        rows, cols = int(t.shape[0]), int(t.shape[1])
+        if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+            raise ValueError(f"{what}: {name}'s rows must be contiguous and apart")
+        return int(t.stride(0)) if rows > 1 else cols
+
+    def quantize_rows(self, x, q, scale, pos=None, stream=None) -> None:
+        """int8 rows with one scale a token: scale = max |x| / 127, q the nearest integers to x / scale.
+        x: T x K float32, float16 or bfloat16; q: R x K int8; scale: R float32. pos (T x k int32, from
+        moe_sort): token t goes to the rows pos[t], else to row t. Rows without a token are left."""
+        what = "quantize_rows"
+        ldx, ldq = self._tensor(what, "x", x, (None, None)), self._tensor(what, "q", q, (None, x.shape[1]), "int8")
+        T, K, R, k = int(x.shape[0]), int(x.shape[1]), int(q.shape[0]), 0
+        self._tensor(what, "scale", scale, (R,), "float32")
+        if pos is not None:
+            self._tensor(what, "pos", pos, (T, None), "int32", dense=True)
+            k = int(pos.shape[1])
+        self._check(self._L.fp_quantize_rows(self.h, _ptr(x), _real(what, "x", x), T, K, ldx, _ptr(pos), k, R, _ptr(q),
+                                             ldq, _ptr(scale), self._op_stream(stream)), "fp_quantize_rows")
+
+    def matmul_i8(self, w, x, y, w_scale, x_scale, offsets=None, stream=None) -> None:
+        """y[n][m] = x_scale[n] w_scale[e][m] sum_k w[e][m][k] x[n][k]. w: M x K int8 and w_scale: M, or
+        with offsets (E + 1 int32, from moe_sort) E x M x K and E x M: expert e has the rows
+        offsets[e] .. offsets[e + 1] - 1. x: N x K int8; x_scale: N float32; y: N x M float32, float16 or
+        bfloat16; rows of y that no expert has are left."""
+        what = "matmul_i8"
+        if offsets is None:
+            ldw, E = self._tensor(what, "w", w, (None, None), "int8"), 1
+        else:
+            self._tensor(what, "w", w, (None, None, None), "int8")
+            ldw, E = int(w.shape[2]), int(w.shape[0])
+            self._tensor(what, "offsets", offsets, (E + 1,), "int32")
+        M, K, N = int(w.shape[-2]), int(w.shape[-1]), int(x.shape[0])
+        self._tensor(what, "w_scale", w_scale, w.shape[:-1], "float32", dense=True)
+        ldx = self._tensor(what, "x", x, (None, K), "int8")
+        self._tensor(what, "x_scale", x_scale, (N,), "float32")
+        ldy = self._tensor(what, "y", y, (N, M))
+        self._check(self._L.fp_matmul_i8(self.h, _ptr(w), ldw, _ptr(w_scale), E, M, K, _ptr(x), ldx, _ptr(x_scale), N,
+                                         _ptr(offsets), _ptr(y), _real(what, "y", y), ldy, self._op_stream(stream)),
+                    "fp_matmul_i8")
+
+    def moe_sort(self, e, E: int, offsets, pos, stream=None) -> None:
+        """Tokens sorted by expert. e: T x k (or T) int32, every token's experts, outside [0, E) for none;
+        offsets: E + 1 int32 and pos: int32 of e's shape are written: the experts' first rows, and the row
+        of every choice (by expert, then in the order of the choices; -1 for none)."""
+        what = "moe_sort"
+        self._tensor(what, "e", e, e.shape, "int32", dense=True)
+        self._tensor(what, "offsets", offsets, (E + 1,), "int32")
+        self._tensor(what, "pos", pos, e.shape, "int32", dense=True)
+        self._check(self._L.fp_moe_sort(self.h, _ptr(e), int(e.numel()), int(E), _ptr(offsets), _ptr(pos),
+                                        self._op_stream(stream)), "fp_moe_sort")
+
+    def moe_dispatch(self, x, pos, rows, stream=None) -> None:
+        """rows[pos[t][j]] = x[t]. x: T x K of any type; pos: T x k int32; rows: R x K of x's type. The
+        experts' inputs of prove_dispatch, for any k. Rows without a token are left. Its gradient is
+        moe_combine without weights."""
+        what = "moe_dispatch"
+        ldx = self._tensor(what, "x", x, (None, None))
+        ldr = self._tensor(what, "rows", rows, (None, x.shape[1]), _dtype(x))
+        T, K = int(x.shape[0]), int(x.shape[1])
+        self._tensor(what, "pos", pos, (T, None), "int32", dense=True)
+        size = int(x.element_size())
+        self._check(self._L.fp_moe_dispatch(self.h, _ptr(x), T, K * size, ldx * size, _ptr(pos), int(pos.shape[1]),
+                                            int(rows.shape[0]), _ptr(rows), ldr * size, self._op_stream(stream)),
+                    "fp_moe_dispatch")
+
+    def moe_combine(self, rows, pos, out, weights=None, base=None, stream=None) -> None:
+        """out[t] = base[t] + sum_j weights[t][j] rows[pos[t][j]] (fp32 sums). rows: R x M and out: T x M
+        float32, float16 or bfloat16; pos: T x k int32; weights: T x k float32 or None (ones); base: as out
+        (it may be out) or None."""
+        what = "moe_combine"
+        ldr, ldo = self._tensor(what, "rows", rows, (None, None)), self._tensor(what, "out", out, (None, rows.shape[1]))
+        R, M, T = int(rows.shape[0]), int(rows.shape[1]), int(out.shape[0])
+        self._tensor(what, "pos", pos, (T, None), "int32", dense=True)
+        k = int(pos.shape[1])
+        if weights is not None:
+            self._tensor(what, "weights", weights, (T, k), "float32", dense=True)
+        ldb = self._tensor(what, "base", base, (T, M), _dtype(out)) if base is not None else 0
+        self._check(self._L.fp_moe_combine(self.h, _ptr(rows), _real(what, "rows", rows), R, ldr, _ptr(pos),
+                                           _ptr(weights), _ptr(base), ldb, T, k, M, _ptr(out), _real(what, "out", out),
+                                           ldo, self._op_stream(stream)), "fp_moe_combine")
+
+    def moe_combine_grad(self, dout, rows, pos, weights=None, drows=None, dweights=None, stream=None) -> None:
+        """Gradients of moe_combine: drows[pos[t][j]] = weights[t][j] dout[t] (rows' type) and
+        dweights[t][j] = <dout[t], rows[pos[t][j]]> (T x k float32), either of them None when it is not
+        wanted. dout: T x M (base's gradient as it is). Rows of drows without a choice are left."""
+        what = "moe_combine_grad"
+        ldd, ldr = self._tensor(what, "dout", dout, (None, None)), self._tensor(what, "rows", rows, (None, dout.shape[1]))
+        T, M, R = int(dout.shape[0]), int(dout.shape[1]), int(rows.shape[0])
+        self._tensor(what, "pos", pos, (T, None), "int32", dense=True)
+        k = int(pos.shape[1])
+        for name, t in (("weights", weights), ("dweights", dweights)):
+            if t is not None:
+                self._tensor(what, name, t, (T, k), "float32", dense=True)
+        lddr = self._tensor(what, "drows", drows, (R, M), _dtype(rows)) if drows is not None else 0
+        self._check(self._L.fp_moe_combine_grad(self.h, _ptr(dout), _real(what, "dout", dout), ldd, _ptr(rows),
+                                                _real(what, "rows", rows), R, ldr, _ptr(pos), _ptr(weights), T, k, M,
+                                                _ptr(drows), lddr, _ptr(dweights), self._op_stream(stream)),
+                    "fp_moe_combine_grad")
+
     def last_point(self):
         """(r_row, rho) of the last matmul section proven with this context (host integers)."""
         vr, n = C.c_int32(0), C.c_int32(0)
@@ -1089,7 +1232,7 @@ class Context:
 
     def kernel_stats(self) -> dict:
         """{kernel name: (launches, total ms, algorithmic bytes)} since the last reset."""
-        cap = 64
+        cap = len(kernel_names())
         arr = (_KStat * cap)()
         n = self._check(self._L.fp_kernel_stats(self.h, arr, cap), "fp_kernel_stats")
         out = {}

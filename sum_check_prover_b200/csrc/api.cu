@@ -411,7 +411,8 @@ const char* fp_kernel_name(int k) {
         "route_witness", "route_vectors", "route_open", "route_round", "route_final",
         "lhi2_column", "lhi2_round", "lhi2_final", "silu2_tree", "silu2_round", "silu2_leaf",
         "lu2_hist", "lu2_tree", "lu2_round", "lu2_leaf", "lhr_column", "lhr_round", "lhr_final", "dsp_claim",
-        "dsp_vectors", "silu_inputs", "ffn_hidden", "scl_group"};
+        "dsp_vectors", "silu_inputs", "ffn_hidden", "scl_group", "quant_rows", "matmul_i8", "moe_sort", "moe_dispatch",
+        "moe_combine", "moe_grad"};
     return (k >= 0 && k < K_COUNT) ? names[k] : "?";
 }
 

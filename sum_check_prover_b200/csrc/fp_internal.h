@@ -74,6 +74,12 @@ enum FpKernel {
     K_SILU_INPUTS,
     K_FFN_HIDDEN,
     K_SCL_GROUP,
+    K_QUANT_ROWS,
+    K_MATMUL_I8,
+    K_MOE_SORT,
+    K_MOE_DISPATCH,
+    K_MOE_COMBINE,
+    K_MOE_GRAD,
     K_COUNT
 };
 

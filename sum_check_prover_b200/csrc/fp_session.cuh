@@ -27,7 +27,8 @@ struct alignas(64) FpMailbox {
     volatile uint64_t pad0;
     volatile uint64_t res_seq;    // unused (results are recognised by their slots)
     volatile uint64_t err;        // device -> host: nonzero = a wait gave up
-    volatile uint64_t pad1[2];
+    volatile uint64_t op_err;     // device -> host: nonzero = a wait of a queued operator gave up (kept until read)
+    volatile uint64_t pad1;
     volatile uint64_t res[16];
 };
 

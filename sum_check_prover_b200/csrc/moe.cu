@@ -1,0 +1,429 @@
+// Tokens to their experts and back: fp_moe_sort, fp_moe_dispatch, fp_moe_combine, fp_moe_combine_grad.
+//
+// A layer of E experts takes every token's k choices e[t][j]. Choice i = t k + j has the row
+//   pos_i = #{i' : e_i' < e_i} + #{i' < i : e_i' = e_i}
+// among the experts' inputs: the experts one after the other, each one's rows in the order of the
+// choices (with k = 1 the order of the dispatch statement). The rows go out with
+//   rows[pos[t][j]] = x[t]                                  (dispatch)
+// and come back with
+//   out[t] = base[t] + sum_j weights[t][j] rows[pos[t][j]]  (combine).
+// The gradients are the same movements: a dispatched row's back to its token is a combine without
+// weights, a combine's are d rows[pos[t][j]] = weights[t][j] dout[t] and
+// d weights[t][j] = <dout[t], rows[pos[t][j]]>. Every one of them goes by tokens: a token's k rows are
+// read or written by the threads that own the token, so sums have one order and nothing is atomic.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "fp_ops.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+// ---- sort -----------------------------------------------------------------------------------
+//
+// One thread-block cluster ranks all choices. Warp w of the cluster takes a run of consecutive
+// choices and counts them by expert in a histogram of its own in shared memory; the histograms'
+// prefix sums (over a block's warps, then over the cluster's blocks through distributed shared
+// memory, then over the experts) give every warp the first row of each expert that is its own, and a
+// second pass over its run hands them out. The lanes of a warp that hold the same expert are found by
+// match.any; the order within a warp is the lanes', so the sort is stable.
+constexpr int MS_HIST_BYTES = 176 * 1024;
+constexpr int MS_MAX_CLUSTER = 8;
+
+__global__ void __launch_bounds__(1024)
+    moe_sort_kernel(const int32_t* __restrict__ e, int64_t n, int E, int warps, int32_t* __restrict__ offsets,
+                    int32_t* __restrict__ pos) {
+    cg::cluster_group cl = cg::this_cluster();
+    const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    extern __shared__ int32_t ms_smem[];
+    int32_t* hist = ms_smem;             // warps x E
+    int32_t* tot = hist + warps * E;     // this block's choices of every expert (read by the cluster)
+    int32_t* first = tot + E;            // first row of every expert for this block
+    __shared__ int32_t wsum[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nthr = blockDim.x;
+
+    for (int i = tid; i < warps * E; i += nthr) hist[i] = 0;
+    __syncthreads();
+    // this warp's run of choices, a multiple of 32
+    const int64_t run = ((n + (int64_t)C * warps - 1) / ((int64_t)C * warps) + 31) / 32 * 32;
+    const int64_t lo = min(n, ((int64_t)rank * warps + warp) * run), hi = min(n, lo + run);
+    int32_t* mine = hist + warp * E;
+    if (warp < warps) {
+        for (int64_t i = lo; i < hi; i += 32) {
+            const int32_t x = i + lane < hi ? e[i + lane] : -1;
+            const bool ok = x >= 0 && x < E;
+            const uint32_t same = __match_any_sync(0xffffffffu, ok ? x : -1);
+            if (ok && lane == __ffs(same) - 1) mine[x] += __popc(same);
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    for (int x = tid; x < E; x += nthr) {
+        int32_t s = 0;
+        for (int w = 0; w < warps; w++) {
+            const int32_t h = hist[w * E + x];
+            hist[w * E + x] = s;
+            s += h;
+        }
+        tot[x] = s;
+    }
+    cl.sync();
+    // experts in runs of `per` for every thread: the cluster's total of each, and its share below this block
+    const int per = (E + nthr - 1) / nthr, x0 = min(E, tid * per), x1 = min(E, x0 + per);
+    int32_t sum = 0;
+    for (int x = x0; x < x1; x++) {
+        int32_t below = 0, all = 0;
+        for (int b = 0; b < C; b++) {
+            const int32_t v = cl.map_shared_rank(tot, b)[x];
+            all += v;
+            below += b < rank ? v : 0;
+        }
+        first[x] = sum + below;
+        sum += all;
+        if (rank == 0) offsets[x + 1] = sum;  // within the thread's run; the runs before it are added below
+    }
+    int32_t inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int32_t before = inc - sum;
+    for (int w = 0; w < warp; w++) before += wsum[w];
+    for (int x = x0; x < x1; x++) {
+        first[x] += before;
+        if (rank == 0) offsets[x + 1] += before;
+    }
+    if (rank == 0 && tid == 0) offsets[0] = 0;
+    cl.sync();  // every block has read the others' counts; `first` is complete
+    if (warp < warps) {
+        for (int64_t i = lo; i < hi; i += 32) {
+            const int32_t x = i + lane < hi ? e[i + lane] : -1;
+            const bool ok = x >= 0 && x < E;
+            const uint32_t same = __match_any_sync(0xffffffffu, ok ? x : -1);
+            int32_t p = -1;
+            if (ok) p = first[x] + mine[x] + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (ok && lane == __ffs(same) - 1) mine[x] += __popc(same);
+            __syncwarp();
+            if (i + lane < hi) pos[i + lane] = p;
+        }
+    }
+}
+
+// ---- dispatch -------------------------------------------------------------------------------
+
+// rows[pos[t][j]] = x[t] in units of VT; one token per tpr threads, blockIdx.y a share of the columns
+template <typename VT>
+__global__ void __launch_bounds__(256)
+    moe_dispatch_kernel(const char* __restrict__ x, int64_t T, int64_t nvec, int64_t ldx, const int32_t* __restrict__ pos,
+                        int k, int64_t R, char* __restrict__ rows, int64_t ldr, int tpr) {
+    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    if (t >= T) return;
+    const VT* src = reinterpret_cast<const VT*>(x + t * ldx);
+    const int64_t step = (int64_t)tpr * gridDim.y;
+    for (int64_t c = threadIdx.x % tpr + (int64_t)tpr * blockIdx.y; c < nvec; c += step) {
+        const VT v = src[c];
+        for (int j = 0; j < k; j++) {
+            const int64_t p = pos[t * k + j];
+            if (p >= 0 && p < R) reinterpret_cast<VT*>(rows + p * ldr)[c] = v;
+        }
+    }
+}
+
+template <typename VT>
+void launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, int64_t ldx, const int32_t* pos, int k,
+                     int64_t R, void* rows, int64_t ldr, cudaStream_t st) {
+    const int64_t nvec = bytes / (int64_t)sizeof(VT);
+    int tpr = 32;
+    while (tpr < 256 && tpr < nvec) tpr *= 2;
+    const int rpb = 256 / tpr;
+    const int64_t gx = (T + rpb - 1) / rpb;
+    // few tokens: their columns over more blocks
+    const int64_t gy = std::max<int64_t>(1, std::min((nvec + tpr - 1) / tpr, 4 * (int64_t)c->num_sms / gx));
+    moe_dispatch_kernel<VT><<<dim3((unsigned)gx, (unsigned)gy), 256, 0, st>>>((const char*)x, T, nvec, ldx, pos, k, R,
+                                                                             (char*)rows, ldr, tpr);
+}
+
+// ---- combine --------------------------------------------------------------------------------
+
+// out[t] = base[t] + sum_j w[t][j] rows[pos[t][j]] in fp32, rounded once; V elements per load
+template <typename RT, typename OT, int V>
+__global__ void __launch_bounds__(256)
+    moe_combine_kernel(const RT* __restrict__ rows, int64_t R, int64_t ldr, const int32_t* __restrict__ pos,
+                       const float* __restrict__ w, const OT* base, int64_t ldb, int64_t T, int k, int64_t M, OT* out,
+                       int64_t ldo, int tpr) {
+    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    if (t >= T) return;
+    const int64_t nvec = M / V, step = (int64_t)tpr * gridDim.y;
+    for (int64_t c = threadIdx.x % tpr + (int64_t)tpr * blockIdx.y; c < nvec; c += step) {
+        float acc[V];
+        if (base) {
+            const FpVec<OT, V> b = *reinterpret_cast<const FpVec<OT, V>*>(base + t * ldb + c * V);
+#pragma unroll
+            for (int i = 0; i < V; i++) acc[i] = fp_to_f(b.v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++) acc[i] = 0.0f;
+        }
+        for (int j = 0; j < k; j++) {
+            const int64_t p = pos[t * k + j];
+            if (p < 0 || p >= R) continue;
+            const float s = w ? w[t * k + j] : 1.0f;
+            const FpVec<RT, V> v = *reinterpret_cast<const FpVec<RT, V>*>(rows + p * ldr + c * V);
+#pragma unroll
+            for (int i = 0; i < V; i++) acc[i] = fmaf(s, fp_to_f(v.v[i]), acc[i]);
+        }
+        FpVec<OT, V> o;
+#pragma unroll
+        for (int i = 0; i < V; i++) o.v[i] = fp_from_f<OT>(acc[i]);
+        *reinterpret_cast<FpVec<OT, V>*>(out + t * ldo + c * V) = o;
+    }
+}
+
+// ---- gradients of combine -------------------------------------------------------------------
+
+// One token per block: its k rows' gradients and the k inner products (fp32, a fixed order: a thread's
+// columns, then the block's tree)
+template <typename RT, typename OT, int V>
+__global__ void __launch_bounds__(256)
+    moe_grad_kernel(const OT* __restrict__ dout, int64_t ldd, const RT* __restrict__ rows, int64_t R, int64_t ldr,
+                    const int32_t* __restrict__ pos, const float* __restrict__ w, int64_t T, int k, int64_t M,
+                    RT* __restrict__ drows, int64_t lddr, float* __restrict__ dw) {
+    __shared__ float red[8];
+    const int64_t t = blockIdx.x, nvec = M / V;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int j = 0; j < k; j++) {
+        const int64_t p = pos[t * k + j];
+        const bool ok = p >= 0 && p < R;
+        float dot = 0.0f;
+        if (ok) {
+            const float s = w ? w[t * k + j] : 1.0f;
+            for (int64_t c = threadIdx.x; c < nvec; c += blockDim.x) {
+                const FpVec<OT, V> g = *reinterpret_cast<const FpVec<OT, V>*>(dout + t * ldd + c * V);
+                if (dw) {
+                    const FpVec<RT, V> v = *reinterpret_cast<const FpVec<RT, V>*>(rows + p * ldr + c * V);
+#pragma unroll
+                    for (int i = 0; i < V; i++) dot = fmaf(fp_to_f(g.v[i]), fp_to_f(v.v[i]), dot);
+                }
+                if (drows) {
+                    FpVec<RT, V> o;
+#pragma unroll
+                    for (int i = 0; i < V; i++) o.v[i] = fp_from_f<RT>(s * fp_to_f(g.v[i]));
+                    *reinterpret_cast<FpVec<RT, V>*>(drows + p * lddr + c * V) = o;
+                }
+            }
+        }
+        if (dw) {
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+            __syncthreads();  // red may still be read for the choice before
+            if (lane == 0) red[warp] = dot;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                float a = 0.0f;
+                for (int i = 0; i < (int)(blockDim.x >> 5); i++) a += red[i];
+                dw[t * k + j] = ok ? a : 0.0f;
+            }
+        }
+    }
+}
+
+template <typename F>
+void by_type(int type, F&& f) {
+    if (type == FP_F32)
+        f((float*)nullptr);
+    else if (type == FP_F16)
+        f((__half*)nullptr);
+    else
+        f((__nv_bfloat16*)nullptr);
+}
+
+// positions: T x k of them, rows 0 .. R - 1
+int check_positions(fp_ctx* c, const char* what, int64_t T, int k, int64_t R) {
+    if (T < 0 || T > (1ll << 24) || R < 0 || R > 0x7fffffffll)
+        return fp_fail(c, FP_ERR_SHAPE, std::string(what) + ": T outside [0, 2^24] or R outside [0, 2^31)");
+    if (k < 1 || T * k > 0x7fffffffll) return fp_fail(c, FP_ERR_SHAPE, std::string(what) + ": k < 1 or T k above 2^31 - 1");
+    return FP_OK;
+}
+
+}  // namespace
+
+int fp_moe_sort(fp_ctx* c, const int32_t* e, int64_t n, int E, int32_t* offsets, int32_t* pos, void* stream) {
+    if (n < 0 || n > 0x7fffffffll || E < 1 || E > 4096)
+        return fp_fail(c, FP_ERR_SHAPE, "fp_moe_sort: n outside [0, 2^31) or E outside [1, 4096]");
+    if (!offsets || (n && (!e || !pos))) return fp_fail(c, FP_ERR_ARG, "fp_moe_sort: null argument");
+    if (((uintptr_t)e | (uintptr_t)offsets | (uintptr_t)pos) % 4)
+        return fp_fail(c, FP_ERR_ARG, "fp_moe_sort: an address is not a multiple of its element size");
+    if (!c) return FP_ERR_ARG;
+    FpDeviceScope dev(c);
+    if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_moe_sort");
+    cudaStream_t st = (cudaStream_t)stream;
+    // as many warps as have 32 choices each: one block, then a cluster of up to eight
+    const int64_t need = std::max<int64_t>(1, (n + 31) / 32);
+    const int most = (int)std::min<int64_t>(32, MS_HIST_BYTES / (4 * (int64_t)E));
+    int blocks = 1;
+    while (blocks < MS_MAX_CLUSTER && need > (int64_t)blocks * most) blocks *= 2;
+    const int warps = (int)std::min<int64_t>(most, (need + blocks - 1) / blocks);
+    const int threads = std::max(32 * warps, 128);
+    const size_t smem = sizeof(int32_t) * ((size_t)warps * E + 2 * (size_t)E);
+    FP_CUDA(c, cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MS_HIST_BYTES + 8 * 4096));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)blocks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int slot;
+    fp_op_tic(c, st, K_MOE_SORT, 8.0 * (double)n + 4.0 * E, &slot);
+    const cudaError_t rc = cudaLaunchKernelEx(&cfg, moe_sort_kernel, e, n, E, warps, offsets, pos);
+    fp_toc(c, st, slot);
+    FP_CUDA(c, rc);
+    return FP_OK;
+}
+
+int fp_moe_dispatch(fp_ctx* c, const void* x, int64_t T, int64_t row_bytes, int64_t ldx, const int32_t* pos, int k,
+                    int64_t R, void* rows, int64_t ldr, void* stream) {
+    int rc = check_positions(c, "fp_moe_dispatch", T, k, R);
+    if (rc) return rc;
+    if (row_bytes < 1 || row_bytes > (1ll << 24)) return fp_fail(c, FP_ERR_SHAPE, "fp_moe_dispatch: row_bytes outside [1, 2^24]");
+    if ((T > 1 && ldx < row_bytes) || (R > 1 && ldr < row_bytes))
+        return fp_fail(c, FP_ERR_SHAPE, "fp_moe_dispatch: a row pitch below row_bytes");
+    const bool empty = T == 0 || R == 0;
+    if (!empty && (!x || !pos || !rows)) return fp_fail(c, FP_ERR_ARG, "fp_moe_dispatch: null argument");
+    if ((uintptr_t)pos % 4) return fp_fail(c, FP_ERR_ARG, "fp_moe_dispatch: an address is not a multiple of its element size");
+    if (!c) return FP_ERR_ARG;
+    if (empty) return FP_OK;
+    FpDeviceScope dev(c);
+    if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_moe_dispatch");
+    cudaStream_t st = (cudaStream_t)stream;
+    if (T == 1) ldx = 0;
+    if (R == 1) ldr = 0;
+    const int al = fp_common_align({(uint64_t)(uintptr_t)x, (uint64_t)(uintptr_t)rows, (uint64_t)ldx, (uint64_t)ldr,
+                                    (uint64_t)row_bytes});
+    int slot;
+    fp_op_tic(c, st, K_MOE_DISPATCH, (double)row_bytes * (T + T * (double)k) + 4.0 * T * k, &slot);
+    if (al >= 16)
+        launch_dispatch<uint4>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+    else if (al >= 8)
+        launch_dispatch<uint2>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+    else if (al >= 4)
+        launch_dispatch<uint32_t>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+    else if (al >= 2)
+        launch_dispatch<uint16_t>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+    else
+        launch_dispatch<uint8_t>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+    fp_toc(c, st, slot);
+    FP_CUDA(c, cudaGetLastError());
+    return FP_OK;
+}
+
+int fp_moe_combine(fp_ctx* c, const void* rows, int rows_type, int64_t R, int64_t ldr, const int32_t* pos,
+                   const float* weights, const void* base, int64_t ldb, int64_t T, int k, int64_t M, void* out,
+                   int out_type, int64_t ldo, void* stream) {
+    const int rs = fp_type_size(rows_type), os = fp_type_size(out_type);
+    if (!rs || !os) return fp_fail(c, FP_ERR_ARG, "fp_moe_combine: a type is not FP_F32, FP_F16 or FP_BF16");
+    int rc = check_positions(c, "fp_moe_combine", T, k, R);
+    if (rc) return rc;
+    if (M < 1 || M > (1ll << 24)) return fp_fail(c, FP_ERR_SHAPE, "fp_moe_combine: M outside [1, 2^24]");
+    if ((R > 1 && ldr < M) || (T > 1 && (ldo < M || (base && ldb < M))))
+        return fp_fail(c, FP_ERR_SHAPE, "fp_moe_combine: a row pitch below M");
+    const bool empty = T == 0;
+    if (!empty && ((!rows && R) || !pos || !out)) return fp_fail(c, FP_ERR_ARG, "fp_moe_combine: null argument");
+    if ((uintptr_t)rows % rs || ((uintptr_t)base | (uintptr_t)out) % os || ((uintptr_t)pos | (uintptr_t)weights) % 4)
+        return fp_fail(c, FP_ERR_ARG, "fp_moe_combine: an address is not a multiple of its element size");
+    if (!c) return FP_ERR_ARG;
+    if (empty) return FP_OK;
+    FpDeviceScope dev(c);
+    if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_moe_combine");
+    cudaStream_t st = (cudaStream_t)stream;
+    if (R <= 1) ldr = 0;
+    if (T == 1) ldo = ldb = 0;
+    if (!base) ldb = 0;
+    int slot;
+    fp_op_tic(c, st, K_MOE_COMBINE, (double)M * (rs * (double)T * k + os * (double)T * (base ? 2 : 1)) + 8.0 * T * k, &slot);
+    by_type(rows_type, [&](auto* rp) {
+        using RT = std::remove_pointer_t<decltype(rp)>;
+        by_type(out_type, [&](auto* op) {
+            using OT = std::remove_pointer_t<decltype(op)>;
+            constexpr int V = 16 / sizeof(RT), OA = V * sizeof(OT) < 16 ? V * sizeof(OT) : 16;
+            const bool vec = M % V == 0 && fp_common_align({(uint64_t)(uintptr_t)rows, (uint64_t)ldr * rs}) == 16 &&
+                             fp_common_align({(uint64_t)(uintptr_t)out, (uint64_t)(uintptr_t)base, (uint64_t)ldo * os,
+                                              (uint64_t)ldb * os}) >= OA;
+            const int64_t nvec = vec ? M / V : M;
+            int tpr = 32;
+            while (tpr < 256 && tpr < nvec) tpr *= 2;
+            const int64_t gx = (T + 256 / tpr - 1) / (256 / tpr);
+            const int64_t gy = std::max<int64_t>(1, std::min((nvec + tpr - 1) / tpr, 4 * (int64_t)c->num_sms / gx));
+            const dim3 grid((unsigned)gx, (unsigned)gy);
+            if (vec)
+                moe_combine_kernel<RT, OT, V><<<grid, 256, 0, st>>>((const RT*)rows, R, ldr, pos, weights,
+                                                                    (const OT*)base, ldb, T, k, M, (OT*)out, ldo, tpr);
+            else
+                moe_combine_kernel<RT, OT, 1><<<grid, 256, 0, st>>>((const RT*)rows, R, ldr, pos, weights,
+                                                                    (const OT*)base, ldb, T, k, M, (OT*)out, ldo, tpr);
+        });
+    });
+    fp_toc(c, st, slot);
+    FP_CUDA(c, cudaGetLastError());
+    return FP_OK;
+}
+
+int fp_moe_combine_grad(fp_ctx* c, const void* dout, int out_type, int64_t ldd, const void* rows, int rows_type,
+                        int64_t R, int64_t ldr, const int32_t* pos, const float* weights, int64_t T, int k, int64_t M,
+                        void* drows, int64_t lddr, float* dweights, void* stream) {
+    const int rs = fp_type_size(rows_type), os = fp_type_size(out_type);
+    if (!rs || !os) return fp_fail(c, FP_ERR_ARG, "fp_moe_combine_grad: a type is not FP_F32, FP_F16 or FP_BF16");
+    int rc = check_positions(c, "fp_moe_combine_grad", T, k, R);
+    if (rc) return rc;
+    if (M < 1 || M > (1ll << 24)) return fp_fail(c, FP_ERR_SHAPE, "fp_moe_combine_grad: M outside [1, 2^24]");
+    if ((R > 1 && ((dweights && ldr < M) || (drows && lddr < M))) || (T > 1 && ldd < M))
+        return fp_fail(c, FP_ERR_SHAPE, "fp_moe_combine_grad: a row pitch below M");
+    if (!drows && !dweights) return fp_fail(c, FP_ERR_ARG, "fp_moe_combine_grad: no gradient is asked for");
+    const bool empty = T == 0;
+    if (!empty && (!dout || !pos || (dweights && !rows && R))) return fp_fail(c, FP_ERR_ARG, "fp_moe_combine_grad: null argument");
+    if (((uintptr_t)rows | (uintptr_t)drows) % rs || (uintptr_t)dout % os ||
+        ((uintptr_t)pos | (uintptr_t)weights | (uintptr_t)dweights) % 4)
+        return fp_fail(c, FP_ERR_ARG, "fp_moe_combine_grad: an address is not a multiple of its element size");
+    if (!c) return FP_ERR_ARG;
+    if (empty) return FP_OK;
+    FpDeviceScope dev(c);
+    if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_moe_combine_grad");
+    cudaStream_t st = (cudaStream_t)stream;
+    if (R <= 1 || !dweights) ldr = 0;
+    if (R <= 1 || !drows) lddr = 0;
+    if (T == 1) ldd = 0;
+    const void* rd = dweights ? rows : nullptr;
+    int slot;
+    fp_op_tic(c, st, K_MOE_GRAD,
+              (double)M * (os * (double)T + rs * (double)T * k * ((drows ? 1 : 0) + (dweights ? 1 : 0))) + 12.0 * T * k, &slot);
+    by_type(rows_type, [&](auto* rp) {
+        using RT = std::remove_pointer_t<decltype(rp)>;
+        by_type(out_type, [&](auto* op) {
+            using OT = std::remove_pointer_t<decltype(op)>;
+            constexpr int V = 16 / sizeof(RT), OA = V * sizeof(OT) < 16 ? V * sizeof(OT) : 16;
+            const bool vec = M % V == 0 &&
+                             fp_common_align({(uint64_t)(uintptr_t)rd, (uint64_t)(uintptr_t)drows, (uint64_t)ldr * rs,
+                                              (uint64_t)lddr * rs}) == 16 &&
+                             fp_common_align({(uint64_t)(uintptr_t)dout, (uint64_t)ldd * os}) >= OA;
+            if (vec)
+                moe_grad_kernel<RT, OT, V><<<(unsigned)T, 256, 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos,
+                                                                        weights, T, k, M, (RT*)drows, lddr, dweights);
+            else
+                moe_grad_kernel<RT, OT, 1><<<(unsigned)T, 256, 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos,
+                                                                        weights, T, k, M, (RT*)drows, lddr, dweights);
+        });
+    });
+    fp_toc(c, st, slot);
+    FP_CUDA(c, cudaGetLastError());
+    return FP_OK;
+}
