@@ -788,7 +788,8 @@ int fp_quantize_rows(fp_ctx* ctx, const void* x, int x_type, int64_t T, int64_t 
  *           of bounds.
  *  y        N rows of M values of y_type, pitch ldy.
  * 1 <= M <= 2^24, 0 <= N <= 2^24, 1 <= K < 2^17 (exact int32 sums), 1 <= E <= 4096, E M < 2^31 - 255.
- * Fastest when w, x, ldw and ldx are multiples of 16.
+ * Fastest when w, x, ldw and ldx are multiples of 16. The kernel's waits are bounded: should one run
+ * out, the next call on the context returns FP_ERR_TIMEOUT (once) and the earlier y is not valid.
  */
 int fp_matmul_i8(fp_ctx* ctx, const int8_t* w, int64_t ldw, const float* w_scale, int E, int64_t M, int64_t K,
                  const int8_t* x, int64_t ldx, const float* x_scale, int64_t N, const int32_t* offsets, void* y,

@@ -2,79 +2,596 @@
 //
 // The sum is exact in int32 (K <= 2^17 - 1 keeps 2^14 K below 2^31); the three factors are multiplied in
 // fp32 in the order sum, token scale, channel scale, and rounded to y's type.
+//
+// One kernel on the 5th-generation tensor cores (kind::i8, accumulators in tensor memory). A tile is 128
+// channels of one expert (the MMA's M, tensor-memory lanes) by up to BN of its tokens (the MMA's N, set
+// to the tile's own count rounded up to 16, so a group of three tokens costs a 16-wide MMA). With the
+// weights on the M side a decode step reads every weight once whatever the tokens, and a group's ragged
+// end wastes at most 15 columns. Warps split the work and hand stages over on mbarriers:
+//   warp 0 (one lane)  TMA: per k-tile (128 bytes of K) the weight box (128 rows) and the tokens' boxes
+//                      (XB rows each), 128-byte swizzle: the MMA's K-major layout.
+//   warp 1 (one lane)  four K = 32 MMAs per k-tile, committed to the stage; the tile's last k-tile to the
+//                      accumulator slot's barrier (two slots: the next tile's MMAs run during the epilogue).
+//   warps 2-5          epilogue: tcgen05.ld, both scales, conversion, stores (32 channels of one token a
+//                      warp and store).
+//   warps 6-21         (COPY) operands that TMA cannot read, because their address or pitch is not a multiple
+//                      of 16: four groups of four warps take every fourth k-tile each, read it with word loads,
+//                      realign it in registers and write the same swizzled layout.
+// Blocks are persistent, one per SM, and walk the tiles of all experts (channels fastest, so that blocks
+// that run together share a group's tokens); the experts' tile counts come from the offsets on the device.
+//
+// SPLIT: with fewer tiles than SMs the sum over K of a tile is split among the blocks of a cluster. The
+// blocks exchange their int32 partial sums through distributed shared memory: block d of the cluster
+// finishes the d-th share of the columns. Integer sums have no order, so the split changes no bit.
+//
+// Every wait is bounded; one that runs out sets the context's operator error word, and an abort flag that
+// ends the other roles' waits.
+#include <cuda.h>  // CUtensorMap
+
 #include <algorithm>
 
 #include "fp_ops.cuh"
 
 namespace {
 
-constexpr int MI_TILE = 64;  // channels and tokens per block
-constexpr int MI_BK = 64;    // bytes of K per step
+constexpr int MI_BM = 128;                  // channels per tile
+constexpr int MI_BK = 128;                  // bytes of K per k-tile
+constexpr int MI_W_BYTES = MI_BM * MI_BK;   // the weight box
+constexpr int MI_MAX_STAGES = 12;
+constexpr int MI_SMEM = 220 * 1024;         // dynamic shared memory of a block that has its SM alone
+constexpr int MI_COPY_GROUPS = 4;
+constexpr int MI_BASE_THREADS = 192;
+constexpr uint32_t MI_WAIT_LIMIT = 1u << 24;
 
-struct MiArgs {
+__host__ __device__ constexpr int mi_box_rows(int bn) { return bn >= 256 ? 64 : 32; }  // rows of a token box
+
+struct alignas(64) MiArgs {
+    CUtensorMap tw, tx;  // E M rows of K bytes, boxes of 128 rows; N rows of K bytes, boxes of XB rows
     const int8_t* w;
     const float* w_scale;
     const int8_t* x;
     const float* x_scale;
     const int32_t* offsets;
     void* y;
-    int64_t M, K, N, ldw, ldx, ldy;
-    int E;
+    int64_t ldw, ldx, ldy;
+    int32_t M, K, N, E;
+    int32_t y_type;
+    int32_t copy_w, copy_x;  // (COPY) which operands TMA does not read
+    int32_t mt;              // channel tiles of an expert
+    int32_t nk;              // k-tiles
+    int32_t stages;
+    int32_t per;             // (SPLIT) columns that a block of the cluster finishes
+    volatile uint64_t* err;
 };
 
-// the rows [lo, hi) of expert e, kept inside the N rows and apart from the other experts' whatever the
-// offsets say: each offset counts as the largest up to it (all threads of the block)
-__device__ __forceinline__ void mi_group(const MiArgs& a, int e, int64_t& lo, int64_t& hi) {
-    __shared__ int32_t most;
-    lo = 0;
-    hi = a.N;
-    if (!a.offsets) return;
-    if (threadIdx.x == 0) most = 0;
-    __syncthreads();
-    int32_t m = 0;
-    for (int i = threadIdx.x; i <= e; i += blockDim.x) m = max(m, a.offsets[i]);
-    if (m > 0) atomicMax(&most, m);
-    __syncthreads();
-    lo = min((int64_t)most, a.N);
-    hi = min((int64_t)max(most, a.offsets[e + 1]), a.N);
+__device__ __forceinline__ uint32_t mi_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// K-major operand with the 128-byte swizzle: 8-row x 128-byte atoms 1024 bytes apart
+__device__ __forceinline__ uint64_t mi_desc(uint32_t a) {
+    return (uint64_t)((a >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+           ((uint64_t)2 << 61);
 }
 
-// one block per 64 channels of one expert; it goes over that expert's tokens 64 at a time
-template <typename YT>
-__global__ void __launch_bounds__(256) matmul_i8_kernel(MiArgs a) {
-    __shared__ int32_t sw[MI_TILE][MI_BK / 4 + 1], sx[MI_TILE][MI_BK / 4 + 1];
-    const int e = blockIdx.y, tid = threadIdx.x, tm = tid & 15, tn = tid >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * MI_TILE;
-    int64_t lo, hi;
-    mi_group(a, e, lo, hi);
-    for (int64_t n0 = lo; n0 < hi; n0 += MI_TILE) {
-        int32_t acc[4][4] = {};
-        for (int64_t k0 = 0; k0 < a.K; k0 += MI_BK) {
-            __syncthreads();
-            for (int i = tid; i < MI_TILE * MI_BK; i += 256) {
-                const int r = i / MI_BK, kk = i % MI_BK;
-                const bool in = k0 + kk < a.K;
-                reinterpret_cast<int8_t*>(&sw[r][0])[kk] = in && m0 + r < a.M ? a.w[((int64_t)e * a.M + m0 + r) * a.ldw + k0 + kk] : 0;
-                reinterpret_cast<int8_t*>(&sx[r][0])[kk] = in && n0 + r < hi ? a.x[(n0 + r) * a.ldx + k0 + kk] : 0;
+// byte offset of 16-byte chunk kk of row `row` in that layout
+__device__ __forceinline__ uint32_t mi_off(int row, int kk) {
+    return (row >> 3) * 1024 + (row & 7) * 128 + ((kk ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ void mi_bar_init(uint64_t* b, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(mi_smem(b)), "r"(count) : "memory");
+}
+
+// one bounded wait for a phase; false if it ran out or another role has aborted
+template <bool CLUSTER>
+__device__ __forceinline__ bool mi_wait_scope(uint32_t bar, uint32_t parity, volatile int* abort, volatile uint64_t* err) {
+    for (uint32_t it = 0; it < MI_WAIT_LIMIT; it++) {
+        uint32_t ok;
+        if (CLUSTER)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}\n"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity)
+                : "memory");
+        else
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity)
+                : "memory");
+        if (ok) return true;
+        if (abort && *abort) return false;
+    }
+    if (abort) {
+        *abort = 1;
+        *err = 1;
+        __threadfence_system();
+    }
+    return false;
+}
+__device__ __forceinline__ bool mi_wait(uint32_t bar, uint32_t parity, volatile int* abort, volatile uint64_t* err) {
+    return mi_wait_scope<false>(bar, parity, abort, err);
+}
+__device__ __forceinline__ bool mi_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, volatile uint64_t* err) {
+    return __all_sync(0xffffffffu, mi_wait(bar, parity, abort, err));
+}
+// the same for copies and MMAs in flight while aborting: no flag is looked at
+__device__ __forceinline__ void mi_drain(uint32_t bar, uint32_t parity) { mi_wait_scope<false>(bar, parity, nullptr, nullptr); }
+
+__device__ __forceinline__ void mi_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mi_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mi_mma(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+__device__ __forceinline__ void mi_tma(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];\n" ::"r"(dst),
+        "l"(tm), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mi_ld16(uint32_t a, int32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(a));
+}
+__device__ __forceinline__ void mi_ld8(uint32_t a, int32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(a));
+}
+__device__ __forceinline__ void mi_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+
+// 16 bytes at p, of which the first `valid` (<= 16) are wanted and the others 0: aligned words inside
+// [base, end), the bytes that the operand's rows span, or single bytes at its two ends
+__device__ __forceinline__ uint4 mi_load16(const int8_t* p, int valid, const int8_t* base, const int8_t* end) {
+    uint32_t o[4] = {0, 0, 0, 0};
+    if (valid > 0) {
+        const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3);
+        const int8_t* q = p - sh;
+        if (q >= base && q + 20 <= end) {
+            const uint32_t* qw = reinterpret_cast<const uint32_t*>(q);
+            uint32_t u[5];
+#pragma unroll
+            for (int i = 0; i < 5; i++) u[i] = __ldg(qw + i);
+#pragma unroll
+            for (int i = 0; i < 4; i++) o[i] = __funnelshift_r(u[i], u[i + 1], 8 * sh);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                if (i < valid) o[i >> 2] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
+        }
+        if (valid < 16) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int left = valid - 4 * i;
+                o[i] &= left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
             }
-            __syncthreads();
+        }
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// one k-tile of `rows` rows (r0 the first, those past `lim` zero) into the swizzled layout, by 128 threads
+__device__ __forceinline__ void mi_copy_tile(const int8_t* base, int64_t ld, int64_t total_rows, int64_t r0, int rows,
+                                             int64_t lim, int k0, int K, uint8_t* dst, int t) {
+    const int8_t* end = base + (total_rows - 1) * ld + K;
+    const int kk = t & 7, valid = min(16, K - k0 - 16 * kk);
+#pragma unroll 1
+    for (int r = t >> 3; r < rows; r += 64) {
+        uint4 v[4];
 #pragma unroll
-            for (int q = 0; q < MI_BK / 4; q++)
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++) acc[i][j] = __dp4a(sw[tm + 16 * i][q], sx[tn + 16 * j][q], acc[i][j]);
+        for (int u = 0; u < 4; u++) {
+            const int64_t row = r0 + r + 16 * u;
+            const bool ok = r + 16 * u < rows && row < lim;
+            v[u] = mi_load16(base + (ok ? row * ld + k0 + 16 * kk : 0), ok ? valid : 0, base, end);
         }
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int64_t m = m0 + tm + 16 * i, n = n0 + tn + 16 * j;
-                if (m >= a.M || n >= hi) continue;
-                const float v = (float)acc[i][j] * a.x_scale[n] * a.w_scale[(int64_t)e * a.M + m];
-                reinterpret_cast<YT*>(a.y)[n * a.ldy + m] = fp_from_f<YT>(v);
-            }
+        for (int u = 0; u < 4; u++)
+            if (r + 16 * u < rows) *reinterpret_cast<uint4*>(dst + mi_off(r + 16 * u, kk)) = v[u];
     }
+}
+
+// the tokens of token tile u: expert e's rows [first[e], first[e + 1]) in equal shares of a multiple of 16
+struct MiTokens {
+    int e, n0, cols;
+};
+__device__ __forceinline__ MiTokens mi_tokens(const int32_t* first, const int32_t* tiles, int E, int u) {
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {  // the last expert whose first tile is at or before u: the one that has tile u
+        const int mid = (lo + hi + 1) >> 1;
+        if (tiles[mid] <= u)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int n = first[lo + 1] - first[lo], nt = tiles[lo + 1] - tiles[lo];
+    const int width = ((n + nt - 1) / nt + 15) & ~15, at = (u - tiles[lo]) * width;
+    return MiTokens{lo, first[lo] + at, min(width, n - at)};
+}
+
+// y of 16 columns (tokens n .. n + cols - 1) for one channel
+template <typename YT>
+__device__ __forceinline__ void mi_store16(const MiArgs& a, const int32_t (&v)[16], int64_t n, int cols, int64_t m,
+                                           float ws, bool live, int lane) {
+    const float xl = (lane & 15) < cols ? __ldg(a.x_scale + n + (lane & 15)) : 0.0f;
+    YT* p = reinterpret_cast<YT*>(a.y) + n * a.ldy + m;
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        const float xs = __shfl_sync(0xffffffffu, xl, i);
+        if (live && i < cols) *p = fp_from_f<YT>((float)v[i] * xs * ws);
+        p += a.ldy;
+    }
+}
+
+template <int BN, bool SPLIT, bool COPY>
+__global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS : 0), 1)
+    matmul_i8_kernel(const __grid_constant__ MiArgs a) {
+    constexpr int XB = mi_box_rows(BN);
+    constexpr int STAGE = MI_W_BYTES + BN * MI_BK;
+    constexpr int SLOTS = SPLIT ? 1 : 2;
+    constexpr int TCOLS = SLOTS * BN;
+    extern __shared__ uint8_t mi_raw[];
+    uint8_t* smem = mi_raw + ((1024 - (mi_smem(mi_raw) & 1023)) & 1023);
+    uint8_t* ring = smem;
+    int32_t* red = reinterpret_cast<int32_t*>(ring + a.stages * STAGE);  // (SPLIT) partial sums of the other blocks
+    __shared__ __align__(8) uint64_t full[MI_MAX_STAGES], empty[MI_MAX_STAGES], accfull[2], accempty[2], fin, redfull;
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int s_abort;
+    __shared__ int32_t s_part[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nthr = blockDim.x;
+    const int S = a.stages;
+    uint32_t crank = 0, csize = 1;
+    if (SPLIT) {
+        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
+        asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+    }
+    int32_t* first = reinterpret_cast<int32_t*>(ring + a.stages * STAGE +
+                                                (SPLIT ? (size_t)csize * a.per * MI_BM * sizeof(int32_t) : 0));
+    int32_t* tiles = first + a.E + 1;
+
+    if (tid == 0) {
+        for (int s = 0; s < S; s++) {
+            mi_bar_init(&full[s], 1 + (COPY ? 128 : 0));
+            mi_bar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; s++) {
+            mi_bar_init(&accfull[s], 1);
+            mi_bar_init(&accempty[s], 128);
+        }
+        mi_bar_init(&fin, 1);
+        mi_bar_init(&redfull, SPLIT ? max(1, 4 * ((int)csize - 1)) : 1);
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(mi_smem(&tmem_base)),
+                     "n"(TCOLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    }
+    // the experts' first rows (each offset counted as the largest up to it, inside [0, N]) and the prefix
+    // sums of their token tiles
+    if (!a.offsets) {
+        if (tid == 0) {
+            first[0] = 0;
+            first[1] = a.N;
+        }
+        __syncthreads();
+    } else {
+        const int per = (a.E + nthr) / nthr, x0 = min(a.E + 1, tid * per), x1 = min(a.E + 1, x0 + per);
+        int32_t m = 0;
+        for (int x = x0; x < x1; x++) m = max(m, __ldg(a.offsets + x));
+        int32_t inc = m;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc = max(inc, v);
+        }
+        if (lane == 31) s_part[warp] = inc;
+        __syncthreads();
+        int32_t run = __shfl_up_sync(0xffffffffu, inc, 1);
+        if (lane == 0) run = 0;
+        for (int w = 0; w < warp; w++) run = max(run, s_part[w]);
+        for (int x = x0; x < x1; x++) {
+            run = max(run, __ldg(a.offsets + x));
+            first[x] = min(run, a.N);
+        }
+        __syncthreads();
+    }
+    {
+        const int per = (a.E + nthr - 1) / nthr, x0 = min(a.E, tid * per), x1 = min(a.E, x0 + per);
+        int32_t sum = 0;
+        for (int x = x0; x < x1; x++) sum += (first[x + 1] - first[x] + BN - 1) / BN;
+        int32_t inc = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += v;
+        }
+        if (lane == 31) s_part[warp] = inc;
+        __syncthreads();
+        int32_t run = inc - sum;
+        for (int w = 0; w < warp; w++) run += s_part[w];
+        for (int x = x0; x < x1; x++) {
+            tiles[x] = run;
+            run += (first[x + 1] - first[x] + BN - 1) / BN;
+        }
+        if (x0 < x1 && x1 == a.E) tiles[a.E] = run;
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+    if (SPLIT) {  // the other blocks' barriers are there before anything arrives at them
+        asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;\n" ::: "memory");
+    }
+    const uint32_t tmem = tmem_base;
+    const int total_u = tiles[a.E];  // token tiles; tile (u, m) of channel tile m
+    // this block's (SPLIT: this cluster's) first tile and its step; SPLIT has one tile per cluster
+    const int walkers = SPLIT ? 0x7fffffff : (int)gridDim.x;
+    const int start = SPLIT ? (int)(blockIdx.x / csize) : (int)blockIdx.x;
+    const int u0 = start / a.mt, mm0 = start % a.mt, du = SPLIT ? 0x3fffffff : walkers / a.mt, dm = SPLIT ? 0 : walkers % a.mt;
+    const int kt0 = SPLIT ? (int)((int64_t)a.nk * crank / csize) : 0;
+    const int kt1 = SPLIT ? (int)((int64_t)a.nk * (crank + 1) / csize) : a.nk;
+    volatile uint64_t* err = a.err;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- TMA ----
+            int s = 0;
+            uint32_t ph = 1;  // a fresh barrier's "previous phase" counts as complete
+            uint32_t issued = 0;
+            bool ok = true;
+            for (int u = u0, m = mm0; u < total_u && ok;) {
+                const MiTokens tk = mi_tokens(first, tiles, a.E, u);
+                const int boxes = (tk.cols + XB - 1) / XB;
+                const uint32_t bytes = (COPY && a.copy_w ? 0 : MI_W_BYTES) + (COPY && a.copy_x ? 0 : boxes * XB * MI_BK);
+                const int wrow = tk.e * a.M + m * MI_BM;
+                for (int kt = kt0; kt < kt1; kt++) {
+                    if (!mi_wait(mi_smem(&empty[s]), ph, &s_abort, err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = mi_smem(&full[s]), dst = mi_smem(ring + s * STAGE);
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(fb), "r"(bytes) : "memory");
+                    if (!COPY || !a.copy_w) mi_tma(dst, &a.tw, kt * MI_BK, wrow, fb);
+                    if (!COPY || !a.copy_x)
+                        for (int b = 0; b < boxes; b++)
+                            mi_tma(dst + MI_W_BYTES + b * XB * MI_BK, &a.tx, kt * MI_BK, tk.n0 + b * XB, fb);
+                    issued++;
+                    if (++s == S) s = 0, ph ^= 1;
+                }
+                u += du, m += dm;
+                if (m >= a.mt) m -= a.mt, u++;
+            }
+            if (!ok && !COPY) {
+                // every copy that was issued lands before the block ends (with COPY the copying warps'
+                // arrivals may be missing: the phases never complete, and the bound below waits instead)
+                for (uint32_t i = issued > (uint32_t)S ? issued - S : 0; i < issued; i++)
+                    mi_drain(mi_smem(&full[i % S]), (i / S) & 1u);
+            } else if (!ok) {
+                for (int i = 0; i < 64; i++) __nanosleep(1000000);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---- MMA issue ----
+            int s = 0;
+            uint32_t ph = 0, tc = 0;
+            bool ok = true;
+            for (int u = u0, m = mm0; u < total_u && ok; tc++) {
+                const MiTokens tk = mi_tokens(first, tiles, a.E, u);
+                const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(((tk.cols + 15) & ~15) >> 3) << 17) |
+                                       ((uint32_t)(MI_BM >> 4) << 24);  // s32 += s8 x s8, both K-major
+                const uint32_t slot = tc % SLOTS;
+                if (tc >= SLOTS && !mi_wait(mi_smem(&accempty[slot]), (tc / SLOTS - 1) & 1u, &s_abort, err)) break;
+                asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+                const uint32_t dst = tmem + slot * BN;
+                for (int kt = kt0; kt < kt1; kt++) {
+                    if (!mi_wait(mi_smem(&full[s]), ph, &s_abort, err)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+                    const uint32_t wa = mi_smem(ring + s * STAGE), xa = wa + MI_W_BYTES;
+#pragma unroll
+                    for (int kc = 0; kc < MI_BK / 32; kc++)
+                        mi_mma(dst, mi_desc(wa + kc * 32), mi_desc(xa + kc * 32), idesc, (kt > kt0 || kc > 0) ? 1u : 0u);
+                    mi_commit(mi_smem(&empty[s]));
+                    if (++s == S) s = 0, ph ^= 1;
+                }
+                if (ok) mi_commit(mi_smem(&accfull[slot]));
+                u += du, m += dm;
+                if (m >= a.mt) m -= a.mt, u++;
+            }
+            // every MMA issued is complete before the tensor memory is freed
+            mi_commit(mi_smem(&fin));
+            mi_drain(mi_smem(&fin), 0);
+        }
+        __syncwarp();
+    } else if (warp < 6) {
+        // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31 ----
+        const int qd = warp & 3;
+        uint32_t tc = 0;
+        for (int u = u0, m = mm0; u < total_u; tc++) {
+            const MiTokens tk = mi_tokens(first, tiles, a.E, u);
+            const uint32_t slot = tc % SLOTS;
+            const int64_t row = (int64_t)m * MI_BM + 32 * qd + lane;
+            const bool live = row < a.M;
+            const float ws = live ? __ldg(a.w_scale + (int64_t)tk.e * a.M + row) : 0.0f;
+            if (!mi_wait_warp(mi_smem(&accfull[slot]), (tc / SLOTS) & 1u, &s_abort, err)) break;
+            asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+            const uint32_t base = tmem + ((uint32_t)(32 * qd) << 16) + slot * BN;
+            auto put = [&](const int32_t(&v)[16], int c0, int cols) {
+                if (a.y_type == FP_F32)
+                    mi_store16<float>(a, v, (int64_t)tk.n0 + c0, cols, row, ws, live, lane);
+                else if (a.y_type == FP_F16)
+                    mi_store16<__half>(a, v, (int64_t)tk.n0 + c0, cols, row, ws, live, lane);
+                else
+                    mi_store16<__nv_bfloat16>(a, v, (int64_t)tk.n0 + c0, cols, row, ws, live, lane);
+            };
+            if (!SPLIT) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < tk.cols; c0 += 16) {
+                    int32_t v[16];
+                    mi_ld16(base + (uint32_t)c0, v);
+                    mi_ld_wait();
+                    put(v, c0, min(16, tk.cols - c0));
+                }
+            } else {
+                // send: columns [d per, (d + 1) per) to block d, at [this block][column][lane]
+                const int per = a.per, mrow = 32 * qd + lane;
+                for (uint32_t d = 0; d < csize; d++) {
+                    if (d == crank) continue;
+                    const int lo = (int)d * per, hi = min(tk.cols, lo + per);
+                    uint32_t at;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at)
+                        : "r"(mi_smem(red + (size_t)crank * per * MI_BM + mrow)), "r"(d));
+                    for (int c = lo; c < hi; c += 8) {
+                        int32_t v[8];
+                        mi_ld8(base + (uint32_t)c, v);
+                        mi_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 8; i++)
+                            asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(at + (uint32_t)((c - lo + i) * MI_BM * 4)),
+                                         "r"(v[i])
+                                         : "memory");
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    for (uint32_t d = 0; d < csize; d++) {
+                        if (d == crank) continue;
+                        uint32_t bar;
+                        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(mi_smem(&redfull)), "r"(d));
+                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+                    }
+                }
+                __syncwarp();
+                const bool got =
+                    csize == 1 || __all_sync(0xffffffffu, mi_wait_scope<true>(mi_smem(&redfull), 0, &s_abort, err));
+                if (!got) break;
+                const int lo = (int)crank * per, hi = min(tk.cols, lo + per);
+                for (int c0 = lo; c0 < hi; c0 += 16) {
+                    // (per is a multiple of 8: a share's last 16 columns may be 8 of the next one's, not stored)
+                    int32_t v[16];
+                    mi_ld16(base + (uint32_t)min(c0, BN - 16), v);
+                    mi_ld_wait();
+                    const int shift = c0 - min(c0, BN - 16);  // 0, or 8 at the accumulator's end
+                    if (shift) {
+#pragma unroll
+                        for (int i = 0; i < 8; i++) v[i] = v[i + 8];
+                    }
+                    const int cols = min(16, hi - c0);
+                    for (uint32_t b = 0; b < csize; b++) {
+                        if (b == crank) continue;
+                        const int32_t* src = red + ((size_t)b * per + (c0 - lo)) * MI_BM + mrow;
+#pragma unroll
+                        for (int i = 0; i < 16; i++)
+                            if (i < cols) v[i] += src[i * MI_BM];
+                    }
+                    put(v, c0, cols);
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+            mi_arrive(mi_smem(&accempty[slot]));
+            u += du, m += dm;
+            if (m >= a.mt) m -= a.mt, u++;
+        }
+    } else if (COPY) {
+        // ---- operands that TMA cannot read: group g of four warps fills every MI_COPY_GROUPS-th k-tile ----
+        const int g = (warp - 6) >> 2, t = tid - MI_BASE_THREADS - 128 * g;
+        int s = 0, turn = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int u = u0, m = mm0; u < total_u && ok;) {
+            const MiTokens tk = mi_tokens(first, tiles, a.E, u);
+            const int rows16 = (tk.cols + 15) & ~15;
+            for (int kt = kt0; kt < kt1; kt++) {
+                if (turn == g) {
+                    if (!mi_wait_warp(mi_smem(&empty[s]), ph, &s_abort, err)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* dst = ring + s * STAGE;
+                    if (a.copy_w)
+                        mi_copy_tile(a.w, a.ldw, (int64_t)a.E * a.M, (int64_t)tk.e * a.M + (int64_t)m * MI_BM, MI_BM,
+                                     (int64_t)(tk.e + 1) * a.M, kt * MI_BK, a.K, dst, t);
+                    if (a.copy_x)
+                        mi_copy_tile(a.x, a.ldx, a.N, tk.n0, rows16, (int64_t)tk.n0 + tk.cols, kt * MI_BK, a.K,
+                                     dst + MI_W_BYTES, t);
+                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA reads
+                    mi_arrive(mi_smem(&full[s]));
+                }
+                if (++turn == MI_COPY_GROUPS) turn = 0;
+                if (++s == S) s = 0, ph ^= 1;
+            }
+            u += du, m += dm;
+            if (m >= a.mt) m -= a.mt, u++;
+        }
+    }
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+    if (SPLIT)  // no block leaves while another may still write to it
+        asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;\n" ::: "memory");
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "n"(TCOLS));
+}
+
+template <int BN, bool SPLIT, bool COPY>
+int launch_mi(fp_ctx* c, MiArgs& a, int64_t tiles, int split, cudaStream_t st) {
+    constexpr int STAGE = MI_W_BYTES + BN * MI_BK;
+    a.per = SPLIT ? (((BN + split - 1) / split) + 7) & ~7 : 0;
+    const size_t extra = (SPLIT ? (size_t)split * a.per * MI_BM * 4 : 0) + 8 * ((size_t)a.E + 1) + 1024;
+    a.stages = (int)std::min<size_t>(MI_MAX_STAGES, (MI_SMEM - extra) / STAGE);
+    auto kern = matmul_i8_kernel<BN, SPLIT, COPY>;
+    FP_CUDA(c, cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MI_SMEM));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : std::min<int64_t>(tiles, c->num_sms)));
+    cfg.blockDim = dim3(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS : 0));
+    cfg.dynamicSmemBytes = a.stages * STAGE + extra;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = SPLIT ? 1 : 0;
+    FP_CUDA(c, cudaLaunchKernelEx(&cfg, kern, a));
+    return FP_OK;
+}
+
+// BN by the tokens that a group has, the split by the tiles there are
+template <int BN>
+int launch_bn(fp_ctx* c, MiArgs& a, cudaStream_t st) {
+    // operands whose rows TMA can address; the others are copied by warps
+    a.copy_w = ((uintptr_t)a.w | (uint64_t)a.ldw) % 16 != 0 ||
+               !fp_tmap_u8_2d(&a.tw, a.w, (uint64_t)a.K, (uint64_t)a.E * a.M, (uint64_t)a.ldw, MI_BK, MI_BM, true);
+    a.copy_x = ((uintptr_t)a.x | (uint64_t)a.ldx) % 16 != 0 ||
+               !fp_tmap_u8_2d(&a.tx, a.x, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.ldx, MI_BK, mi_box_rows(BN), true);
+    const bool copy = a.copy_w || a.copy_x;
+    // tiles at most: every group that can have rows has one token tile, and the rows fill the others
+    const int64_t groups = std::min(a.E, a.N);
+    const int64_t tiles = a.mt * (groups == 1 ? (a.N + BN - 1) / BN : groups + a.N / BN);
+    if constexpr (BN <= 128) {
+        int split = 1;
+        while (split < 8 && tiles * split * 2 <= c->num_sms && split * 4 <= a.nk) split *= 2;
+        if (split > 1)
+            return copy ? launch_mi<BN, true, true>(c, a, tiles, split, st) : launch_mi<BN, true, false>(c, a, tiles, split, st);
+    }
+    return copy ? launch_mi<BN, false, true>(c, a, tiles, 1, st) : launch_mi<BN, false, false>(c, a, tiles, 1, st);
 }
 
 }  // namespace
@@ -96,21 +613,28 @@ int fp_matmul_i8(fp_ctx* c, const int8_t* w, int64_t ldw, const float* w_scale, 
     if (((uintptr_t)w_scale | (uintptr_t)x_scale | (uintptr_t)offsets) % 4 || (uintptr_t)y % ys)
         return fp_fail(c, FP_ERR_ARG, "fp_matmul_i8: an address is not a multiple of its element size");
     if (!c) return FP_ERR_ARG;
+    if (c->mb->op_err) {
+        c->mb->op_err = 0;
+        return fp_fail(c, FP_ERR_TIMEOUT, "fp_matmul_i8: a wait of an earlier call ran out on the device; its y is not valid");
+    }
     if (empty) return FP_OK;
     FpDeviceScope dev(c);
     if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_matmul_i8");
     cudaStream_t st = (cudaStream_t)stream;
-    MiArgs a{w, w_scale, x, x_scale, offsets, y, M, K, N, ldw, ldx, ldy, E};
-    const dim3 grid((unsigned)((M + MI_TILE - 1) / MI_TILE), (unsigned)E);
+    if (N == 1) ldx = (K + 15) & ~15ll, ldy = M;  // a single row has no pitch: one that keeps its alignment
+    if (E * M == 1) ldw = (K + 15) & ~15ll;
+    MiArgs a = {};
+    a.w = w, a.w_scale = w_scale, a.x = x, a.x_scale = x_scale, a.offsets = offsets, a.y = y;
+    a.ldw = ldw, a.ldx = ldx, a.ldy = ldy;
+    a.M = (int32_t)M, a.K = (int32_t)K, a.N = (int32_t)N, a.E = E, a.y_type = y_type;
+    a.mt = (int32_t)((M + MI_BM - 1) / MI_BM);
+    a.nk = (int32_t)((K + MI_BK - 1) / MI_BK);
+    a.err = &c->mb_dev->op_err;
+    // rows of a group: N of a dense product, twice the mean of those that can have rows by expert
+    const int64_t rows = E == 1 ? N : 2 * ((N + std::min<int64_t>(E, N) - 1) / std::min<int64_t>(E, N));
     int slot;
-    fp_op_tic(c, st, K_MATMUL_I8, (double)E * M * K + (double)N * (K + ys * (double)M), &slot);
-    if (y_type == FP_F32)
-        matmul_i8_kernel<float><<<grid, 256, 0, st>>>(a);
-    else if (y_type == FP_F16)
-        matmul_i8_kernel<__half><<<grid, 256, 0, st>>>(a);
-    else
-        matmul_i8_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+    fp_op_tic(c, st, K_MATMUL_I8, (double)std::min<int64_t>(E, N) * M * K + (double)N * (K + ys * (double)M), &slot);
+    const int rc = rows <= 32 ? launch_bn<32>(c, a, st) : rows <= 128 ? launch_bn<128>(c, a, st) : launch_bn<256>(c, a, st);
     fp_toc(c, st, slot);
-    FP_CUDA(c, cudaGetLastError());
-    return FP_OK;
+    return rc;
 }
