@@ -49,6 +49,7 @@ class _LRec(C.Structure):
 
 
 _lib = None
+_raw_stream = None  # device -> its current stream's handle
 
 
 def lib():
@@ -623,16 +624,19 @@ def _stream(stream) -> Optional[int]:
 
 
 _REAL = {"float32": 0, "float16": 1, "bfloat16": 2}  # FP_F32, FP_F16, FP_BF16
+_DTYPES: dict = {}  # a tensor's dtype -> (its name, its FP_ type or None): a lookup per tensor and call
 
 
-def _dtype(t) -> str:
-    return str(t.dtype).rsplit(".", 1)[-1]
+def _dtype(dt) -> tuple:
+    got = _DTYPES.get(dt)
+    if got is None:
+        name = str(dt).rsplit(".", 1)[-1]
+        got = _DTYPES[dt] = (name, _REAL.get(name))
+    return got
 
 
-def _real(what: str, name: str, t) -> int:
-    if _dtype(t) not in _REAL:
-        raise ValueError(f"{what}: {name} must be float32, float16 or bfloat16, not {_dtype(t)}")
-    return _REAL[_dtype(t)]
+def _times(shape) -> str:
+    return " x ".join(map(str, shape))
 
 
 class SiteDesc:
@@ -1003,46 +1007,77 @@ class Context:
                                           _ptr(y), _stream(stream)), "fp_ffn_hidden")
 
     # -- operators of the layer around the proven products: kernels queued on the stream (the current
-    # one of the context's device), buffers the caller's --
+    # one of the context's device), buffers the caller's. A decode step makes several calls of a few
+    # microseconds, so the checks look at each tensor's attributes once --
 
     def _op_stream(self, stream) -> Optional[int]:
-        if stream is None:
+        if stream is not None:
+            return _stream(stream)
+        global _raw_stream
+        if _raw_stream is None:
             import torch
-            return int(torch.cuda.current_stream(self.device).cuda_stream)
-        return _stream(stream)
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(self.device)
 
-    def _tensor(self, what: str, name: str, t, shape, dtype: Optional[str] = None, dense: bool = False):
-        """Check a device tensor's type, shape (None: any) and layout; returns its row pitch. Rows of a
-        two-dimensional tensor may be part of wider ones unless it has to be dense."""
-        if t.device.type != "cuda" or t.device.index != self.device:
+    def _at(self, what: str, name: str, t) -> int:
+        """The address of a tensor on the context's device."""
+        if t.get_device() != self.device:
             raise ValueError(f"{what}: {name} must be on cuda:{self.device}, not {t.device}")
-        if dtype is not None and _dtype(t) != dtype:
-            raise ValueError(f"{what}: {name} must be {dtype}, not {_dtype(t)}")
-        if t.dim() != len(shape) or any(a is not None and int(a) != int(b) for a, b in zip(shape, t.shape)):
-            want = " x ".join("?" if a is None else str(int(a)) for a in shape)
-            raise ValueError(f"{what}: {name} must be {want}, not {' x '.join(map(str, t.shape))}")
-        if dense or t.dim() != 2:
-            if not t.is_contiguous():
-                raise ValueError(f"{what}: {name} must be contiguous")
-            return int(t.shape[-1])
-        rows, cols = int(t.shape[0]), int(t.shape[1])
-        if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        return t.data_ptr()
+
+    def _dense(self, what: str, name: str, t, shape: tuple, dtype: str) -> int:
+        """Check a contiguous tensor of one shape and type; its address."""
+        if t.shape != shape:
+            raise ValueError(f"{what}: {name} must be {_times(shape)}, not {_times(t.shape)}")
+        if _dtype(t.dtype)[0] != dtype:
+            raise ValueError(f"{what}: {name} must be {dtype}, not {_dtype(t.dtype)[0]}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+        return self._at(what, name, t)
+
+    def _rows(self, what: str, name: str, t, rows: Optional[int] = None, cols: Optional[int] = None,
+              dtype: Optional[str] = None) -> tuple:
+        """Check a two-dimensional tensor whose rows may be part of wider ones; (address, rows, columns,
+        row pitch)."""
+        shape = t.shape
+        if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
+            want = _times("?" if x is None else x for x in (rows, cols))
+            raise ValueError(f"{what}: {name} must be {want}, not {_times(shape)}")
+        if dtype is not None and _dtype(t.dtype)[0] != dtype:
+            raise ValueError(f"{what}: {name} must be {dtype}, not {_dtype(t.dtype)[0]}")
+        n, m = shape
+        ld, step = t.stride()
+        if (m > 1 and step != 1) or (n > 1 and ld < m):
             raise ValueError(f"{what}: {name}'s rows must be contiguous and apart")
-        return int(t.stride(0)) if rows > 1 else cols
+        return self._at(what, name, t), n, m, (ld if n > 1 else m)
+
+    def _real(self, what: str, name: str, t) -> int:
+        dt, code = _dtype(t.dtype)
+        if code is None:
+            raise ValueError(f"{what}: {name} must be float32, float16 or bfloat16, not {dt}")
+        return code
+
+    def _positions(self, what: str, pos, T: int) -> tuple:
+        """(address, choices a token) of T x k int32 positions."""
+        if len(pos.shape) != 2:
+            raise ValueError(f"{what}: pos must be {T} x ?, not {_times(pos.shape)}")
+        k = pos.shape[1]
+        return self._dense(what, "pos", pos, (T, k), "int32"), k
 
     def quantize_rows(self, x, q, scale, pos=None, stream=None) -> None:
         """int8 rows with one scale a token: scale = max |x| / 127, q the nearest integers to x / scale.
         x: T x K float32, float16 or bfloat16; q: R x K int8; scale: R float32. pos (T x k int32, from
         moe_sort): token t goes to the rows pos[t], else to row t. Rows without a token are left."""
         what = "quantize_rows"
-        ldx, ldq = self._tensor(what, "x", x, (None, None)), self._tensor(what, "q", q, (None, x.shape[1]), "int8")
-        T, K, R, k = int(x.shape[0]), int(x.shape[1]), int(q.shape[0]), 0
-        self._tensor(what, "scale", scale, (R,), "float32")
-        if pos is not None:
-            self._tensor(what, "pos", pos, (T, None), "int32", dense=True)
-            k = int(pos.shape[1])
-        self._check(self._L.fp_quantize_rows(self.h, _ptr(x), _real(what, "x", x), T, K, ldx, _ptr(pos), k, R, _ptr(q),
-                                             ldq, _ptr(scale), self._op_stream(stream)), "fp_quantize_rows")
+        xp, T, K, ldx = self._rows(what, "x", x)
+        xt = self._real(what, "x", x)
+        qp, R, _, ldq = self._rows(what, "q", q, None, K, "int8")
+        sp = self._dense(what, "scale", scale, (R,), "float32")
+        pp, k = self._positions(what, pos, T) if pos is not None else (None, 0)
+        rc = self._L.fp_quantize_rows(self.h, xp, xt, T, K, ldx, pp, k, R, qp, ldq, sp, self._op_stream(stream))
+        if rc:
+            self._check(rc, "fp_quantize_rows")
 
     def matmul_i8(self, w, x, y, w_scale, x_scale, offsets=None, stream=None) -> None:
         """y[n][m] = x_scale[n] w_scale[e][m] sum_k w[e][m][k] x[n][k]. w: M x K int8 and w_scale: M, or
@@ -1051,78 +1086,84 @@ class Context:
         bfloat16; rows of y that no expert has are left."""
         what = "matmul_i8"
         if offsets is None:
-            ldw, E = self._tensor(what, "w", w, (None, None), "int8"), 1
+            wp, M, K, ldw = self._rows(what, "w", w, None, None, "int8")
+            E, op = 1, None
+            wsp = self._dense(what, "w_scale", w_scale, (M,), "float32")
         else:
-            self._tensor(what, "w", w, (None, None, None), "int8")
-            ldw, E = int(w.shape[2]), int(w.shape[0])
-            self._tensor(what, "offsets", offsets, (E + 1,), "int32")
-        M, K, N = int(w.shape[-2]), int(w.shape[-1]), int(x.shape[0])
-        self._tensor(what, "w_scale", w_scale, w.shape[:-1], "float32", dense=True)
-        ldx = self._tensor(what, "x", x, (None, K), "int8")
-        self._tensor(what, "x_scale", x_scale, (N,), "float32")
-        ldy = self._tensor(what, "y", y, (N, M))
-        self._check(self._L.fp_matmul_i8(self.h, _ptr(w), ldw, _ptr(w_scale), E, M, K, _ptr(x), ldx, _ptr(x_scale), N,
-                                         _ptr(offsets), _ptr(y), _real(what, "y", y), ldy, self._op_stream(stream)),
-                    "fp_matmul_i8")
+            shape = w.shape
+            if len(shape) != 3:
+                raise ValueError(f"{what}: w must be experts x channels x K, not {_times(shape)}")
+            E, M, K = shape
+            ldw = K
+            wp = self._dense(what, "w", w, (E, M, K), "int8")
+            wsp = self._dense(what, "w_scale", w_scale, (E, M), "float32")
+            op = self._dense(what, "offsets", offsets, (E + 1,), "int32")
+        xp, N, _, ldx = self._rows(what, "x", x, None, K, "int8")
+        xsp = self._dense(what, "x_scale", x_scale, (N,), "float32")
+        yp, _, _, ldy = self._rows(what, "y", y, N, M)
+        rc = self._L.fp_matmul_i8(self.h, wp, ldw, wsp, E, M, K, xp, ldx, xsp, N, op, yp, self._real(what, "y", y), ldy,
+                                  self._op_stream(stream))
+        if rc:
+            self._check(rc, "fp_matmul_i8")
 
     def moe_sort(self, e, E: int, offsets, pos, stream=None) -> None:
         """Tokens sorted by expert. e: T x k (or T) int32, every token's experts, outside [0, E) for none;
         offsets: E + 1 int32 and pos: int32 of e's shape are written: the experts' first rows, and the row
         of every choice (by expert, then in the order of the choices; -1 for none)."""
         what = "moe_sort"
-        self._tensor(what, "e", e, e.shape, "int32", dense=True)
-        self._tensor(what, "offsets", offsets, (E + 1,), "int32")
-        self._tensor(what, "pos", pos, e.shape, "int32", dense=True)
-        self._check(self._L.fp_moe_sort(self.h, _ptr(e), int(e.numel()), int(E), _ptr(offsets), _ptr(pos),
-                                        self._op_stream(stream)), "fp_moe_sort")
+        shape = e.shape
+        ep = self._dense(what, "e", e, shape, "int32")
+        op = self._dense(what, "offsets", offsets, (E + 1,), "int32")
+        pp = self._dense(what, "pos", pos, shape, "int32")
+        rc = self._L.fp_moe_sort(self.h, ep, e.numel(), E, op, pp, self._op_stream(stream))
+        if rc:
+            self._check(rc, "fp_moe_sort")
 
     def moe_dispatch(self, x, pos, rows, stream=None) -> None:
         """rows[pos[t][j]] = x[t]. x: T x K of any type; pos: T x k int32; rows: R x K of x's type. The
         experts' inputs of prove_dispatch, for any k. Rows without a token are left. Its gradient is
         moe_combine without weights."""
         what = "moe_dispatch"
-        ldx = self._tensor(what, "x", x, (None, None))
-        ldr = self._tensor(what, "rows", rows, (None, x.shape[1]), _dtype(x))
-        T, K = int(x.shape[0]), int(x.shape[1])
-        self._tensor(what, "pos", pos, (T, None), "int32", dense=True)
-        size = int(x.element_size())
-        self._check(self._L.fp_moe_dispatch(self.h, _ptr(x), T, K * size, ldx * size, _ptr(pos), int(pos.shape[1]),
-                                            int(rows.shape[0]), _ptr(rows), ldr * size, self._op_stream(stream)),
-                    "fp_moe_dispatch")
+        xp, T, K, ldx = self._rows(what, "x", x)
+        rp, R, _, ldr = self._rows(what, "rows", rows, None, K, _dtype(x.dtype)[0])
+        pp, k = self._positions(what, pos, T)
+        size = x.element_size()
+        rc = self._L.fp_moe_dispatch(self.h, xp, T, K * size, ldx * size, pp, k, R, rp, ldr * size,
+                                     self._op_stream(stream))
+        if rc:
+            self._check(rc, "fp_moe_dispatch")
 
     def moe_combine(self, rows, pos, out, weights=None, base=None, stream=None) -> None:
         """out[t] = base[t] + sum_j weights[t][j] rows[pos[t][j]] (fp32 sums). rows: R x M and out: T x M
         float32, float16 or bfloat16; pos: T x k int32; weights: T x k float32 or None (ones); base: as out
         (it may be out) or None."""
         what = "moe_combine"
-        ldr, ldo = self._tensor(what, "rows", rows, (None, None)), self._tensor(what, "out", out, (None, rows.shape[1]))
-        R, M, T = int(rows.shape[0]), int(rows.shape[1]), int(out.shape[0])
-        self._tensor(what, "pos", pos, (T, None), "int32", dense=True)
-        k = int(pos.shape[1])
-        if weights is not None:
-            self._tensor(what, "weights", weights, (T, k), "float32", dense=True)
-        ldb = self._tensor(what, "base", base, (T, M), _dtype(out)) if base is not None else 0
-        self._check(self._L.fp_moe_combine(self.h, _ptr(rows), _real(what, "rows", rows), R, ldr, _ptr(pos),
-                                           _ptr(weights), _ptr(base), ldb, T, k, M, _ptr(out), _real(what, "out", out),
-                                           ldo, self._op_stream(stream)), "fp_moe_combine")
+        rp, R, M, ldr = self._rows(what, "rows", rows)
+        op, T, _, ldo = self._rows(what, "out", out, None, M)
+        pp, k = self._positions(what, pos, T)
+        wp = self._dense(what, "weights", weights, (T, k), "float32") if weights is not None else None
+        bp, _, _, ldb = self._rows(what, "base", base, T, M, _dtype(out.dtype)[0]) if base is not None else (None, 0, 0, 0)
+        rc = self._L.fp_moe_combine(self.h, rp, self._real(what, "rows", rows), R, ldr, pp, wp, bp, ldb, T, k, M, op,
+                                    self._real(what, "out", out), ldo, self._op_stream(stream))
+        if rc:
+            self._check(rc, "fp_moe_combine")
 
     def moe_combine_grad(self, dout, rows, pos, weights=None, drows=None, dweights=None, stream=None) -> None:
         """Gradients of moe_combine: drows[pos[t][j]] = weights[t][j] dout[t] (rows' type) and
         dweights[t][j] = <dout[t], rows[pos[t][j]]> (T x k float32), either of them None when it is not
         wanted. dout: T x M (base's gradient as it is). Rows of drows without a choice are left."""
         what = "moe_combine_grad"
-        ldd, ldr = self._tensor(what, "dout", dout, (None, None)), self._tensor(what, "rows", rows, (None, dout.shape[1]))
-        T, M, R = int(dout.shape[0]), int(dout.shape[1]), int(rows.shape[0])
-        self._tensor(what, "pos", pos, (T, None), "int32", dense=True)
-        k = int(pos.shape[1])
-        for name, t in (("weights", weights), ("dweights", dweights)):
-            if t is not None:
-                self._tensor(what, name, t, (T, k), "float32", dense=True)
-        lddr = self._tensor(what, "drows", drows, (R, M), _dtype(rows)) if drows is not None else 0
-        self._check(self._L.fp_moe_combine_grad(self.h, _ptr(dout), _real(what, "dout", dout), ldd, _ptr(rows),
-                                                _real(what, "rows", rows), R, ldr, _ptr(pos), _ptr(weights), T, k, M,
-                                                _ptr(drows), lddr, _ptr(dweights), self._op_stream(stream)),
-                    "fp_moe_combine_grad")
+        dp, T, M, ldd = self._rows(what, "dout", dout)
+        rp, R, _, ldr = self._rows(what, "rows", rows, None, M)
+        pp, k = self._positions(what, pos, T)
+        wp = self._dense(what, "weights", weights, (T, k), "float32") if weights is not None else None
+        dwp = self._dense(what, "dweights", dweights, (T, k), "float32") if dweights is not None else None
+        gp, _, _, ldg = self._rows(what, "drows", drows, R, M, _dtype(rows.dtype)[0]) if drows is not None else (None, 0, 0, 0)
+        rc = self._L.fp_moe_combine_grad(self.h, dp, self._real(what, "dout", dout), ldd, rp,
+                                         self._real(what, "rows", rows), R, ldr, pp, wp, T, k, M, gp, ldg, dwp,
+                                         self._op_stream(stream))
+        if rc:
+            self._check(rc, "fp_moe_combine_grad")
 
     def last_point(self):
         """(r_row, rho) of the last matmul section proven with this context (host integers)."""

@@ -136,6 +136,7 @@ struct fp_ctx {
     // unscaled sites, 0 mma.sync (FP_TCGEN05 selects 0 or 1)
     int tc_gemm = 2;
     FpMmPoint mm_point;
+    uint32_t op_smem = 0;  // operator kernels whose shared-memory limit has been raised on this device, a bit each
     // timing
     int profiling = 0;
     int64_t launches = 0;  // every kernel launch of the library on this context

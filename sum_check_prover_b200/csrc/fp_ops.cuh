@@ -40,6 +40,15 @@ static inline void fp_op_tic(fp_ctx* c, cudaStream_t s, int kernel, double bytes
     fp_tic(c, s, kernel, bytes, slot);
 }
 
+// raises a kernel's limit of dynamic shared memory, once a context (bit: the kernel's number)
+template <typename F>
+static inline cudaError_t fp_op_smem(fp_ctx* c, int bit, F* kernel, int bytes) {
+    if (c->op_smem >> bit & 1) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) c->op_smem |= 1u << bit;
+    return e;
+}
+
 // the largest power of two, at most 16, that divides every given address or pitch
 static inline int fp_common_align(std::initializer_list<uint64_t> v) {
     uint64_t a = 16;

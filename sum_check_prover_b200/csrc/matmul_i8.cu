@@ -8,9 +8,9 @@
 // to the tile's own count rounded up to 16, so a group of three tokens costs a 16-wide MMA). With the
 // weights on the M side a decode step reads every weight once whatever the tokens, and a group's ragged
 // end wastes at most 15 columns. Warps split the work and hand stages over on mbarriers:
-//   warp 0 (one lane)  TMA: per k-tile (128 bytes of K) the weight box (128 rows) and the tokens' boxes
+//   warp 0             TMA: per k-tile (128 bytes of K) the weight box (128 rows) and the tokens' boxes
 //                      (XB rows each), 128-byte swizzle: the MMA's K-major layout.
-//   warp 1 (one lane)  four K = 32 MMAs per k-tile, committed to the stage; the tile's last k-tile to the
+//   warp 1             four K = 32 MMAs per k-tile, committed to the stage; the tile's last k-tile to the
 //                      accumulator slot's barrier (two slots: the next tile's MMAs run during the epilogue).
 //   warps 2-5          epilogue: tcgen05.ld, both scales, conversion, stores (32 channels of one token a
 //                      warp and store).
@@ -66,10 +66,16 @@ struct alignas(64) MiArgs {
 
 __device__ __forceinline__ uint32_t mi_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// K-major operand with the 128-byte swizzle: 8-row x 128-byte atoms 1024 bytes apart
-__device__ __forceinline__ uint64_t mi_desc(uint32_t a) {
-    return (uint64_t)((a >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-           ((uint64_t)2 << 61);
+// K-major operand with the 128-byte swizzle: 8-row x 128-byte atoms 1024 bytes apart. The low word holds
+// the address / 16 (and a 1 at bit 16), so that a later stage or K step is an addition to it.
+__device__ __forceinline__ uint32_t mi_desc_lo(uint32_t a) { return ((a >> 4) & 0x3FFF) | (1u << 16); }
+constexpr uint32_t MI_DESC_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
+
+// true in one lane of a converged warp, always the same one
+__device__ __forceinline__ bool mi_elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
 }
 
 // byte offset of 16-byte chunk kk of row `row` in that layout
@@ -124,11 +130,13 @@ __device__ __forceinline__ void mi_arrive(uint32_t bar) {
 __device__ __forceinline__ void mi_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mi_mma(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+// a, b: the low words of the operands' descriptors
+__device__ __forceinline__ void mi_mma(uint32_t tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], da, db, %3, p;\n\t}\n" ::"r"(tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(MI_DESC_HI), "r"(add)
         : "memory");
 }
 __device__ __forceinline__ void mi_tma(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
@@ -346,76 +354,84 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
     volatile uint64_t* err = a.err;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---- TMA ----
-            int s = 0;
-            uint32_t ph = 1;  // a fresh barrier's "previous phase" counts as complete
-            uint32_t issued = 0;
-            bool ok = true;
-            for (int u = u0, m = mm0; u < total_u && ok;) {
-                const MiTokens tk = mi_tokens(first, tiles, a.E, u);
-                const int boxes = (tk.cols + XB - 1) / XB;
-                const uint32_t bytes = (COPY && a.copy_w ? 0 : MI_W_BYTES) + (COPY && a.copy_x ? 0 : boxes * XB * MI_BK);
-                const int wrow = tk.e * a.M + m * MI_BM;
-                for (int kt = kt0; kt < kt1; kt++) {
-                    if (!mi_wait(mi_smem(&empty[s]), ph, &s_abort, err)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = mi_smem(&full[s]), dst = mi_smem(ring + s * STAGE);
+        // ---- TMA: the whole warp walks and waits, one lane issues ----
+        const bool lead = mi_elect();
+        const uint32_t full0 = mi_smem(full), empty0 = mi_smem(empty), ring0 = mi_smem(ring);
+        uint32_t s = 0, ph = 1;  // a fresh barrier's "previous phase" counts as complete
+        uint32_t issued = 0;
+        bool ok = true;
+        for (int u = u0, m = mm0; u < total_u && ok;) {
+            const MiTokens tk = mi_tokens(first, tiles, a.E, u);
+            const int boxes = (tk.cols + XB - 1) / XB;
+            const uint32_t bytes = (COPY && a.copy_w ? 0 : MI_W_BYTES) + (COPY && a.copy_x ? 0 : boxes * XB * MI_BK);
+            const int wrow = tk.e * a.M + m * MI_BM;
+            for (int kt = kt0; kt < kt1; kt++) {
+                if (!mi_wait_warp(empty0 + 8 * s, ph, &s_abort, err)) {
+                    ok = false;
+                    break;
+                }
+                if (lead) {
+                    const uint32_t fb = full0 + 8 * s, dst = ring0 + s * STAGE;
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(fb), "r"(bytes) : "memory");
                     if (!COPY || !a.copy_w) mi_tma(dst, &a.tw, kt * MI_BK, wrow, fb);
-                    if (!COPY || !a.copy_x)
-                        for (int b = 0; b < boxes; b++)
-                            mi_tma(dst + MI_W_BYTES + b * XB * MI_BK, &a.tx, kt * MI_BK, tk.n0 + b * XB, fb);
-                    issued++;
-                    if (++s == S) s = 0, ph ^= 1;
+                    if (!COPY || !a.copy_x) {
+#pragma unroll
+                        for (int b = 0; b < BN / XB; b++)
+                            if (b < boxes) mi_tma(dst + MI_W_BYTES + b * XB * MI_BK, &a.tx, kt * MI_BK, tk.n0 + b * XB, fb);
+                    }
                 }
-                u += du, m += dm;
-                if (m >= a.mt) m -= a.mt, u++;
+                issued++;
+                if (++s == (uint32_t)S) s = 0, ph ^= 1;
             }
-            if (!ok && !COPY) {
-                // every copy that was issued lands before the block ends (with COPY the copying warps'
-                // arrivals may be missing: the phases never complete, and the bound below waits instead)
+            u += du, m += dm;
+            if (m >= a.mt) m -= a.mt, u++;
+        }
+        if (!ok && lead) {
+            if (!COPY) {
+                // every copy that was issued lands before the block ends
                 for (uint32_t i = issued > (uint32_t)S ? issued - S : 0; i < issued; i++)
-                    mi_drain(mi_smem(&full[i % S]), (i / S) & 1u);
-            } else if (!ok) {
+                    mi_drain(full0 + 8 * (i % S), (i / S) & 1u);
+            } else {
+                // (the copying warps' arrivals may be missing: the phases never complete, time has to do)
                 for (int i = 0; i < 64; i++) __nanosleep(1000000);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---- MMA issue ----
-            int s = 0;
-            uint32_t ph = 0, tc = 0;
-            bool ok = true;
-            for (int u = u0, m = mm0; u < total_u && ok; tc++) {
-                const MiTokens tk = mi_tokens(first, tiles, a.E, u);
-                const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(((tk.cols + 15) & ~15) >> 3) << 17) |
-                                       ((uint32_t)(MI_BM >> 4) << 24);  // s32 += s8 x s8, both K-major
-                const uint32_t slot = tc % SLOTS;
-                if (tc >= SLOTS && !mi_wait(mi_smem(&accempty[slot]), (tc / SLOTS - 1) & 1u, &s_abort, err)) break;
+        // ---- MMA issue: the same way ----
+        const bool lead = mi_elect();
+        const uint32_t full0 = mi_smem(full), empty0 = mi_smem(empty), desc0 = mi_desc_lo(mi_smem(ring));
+        uint32_t s = 0, ph = 0, tc = 0;
+        bool ok = true;
+        for (int u = u0, m = mm0; u < total_u && ok; tc++) {
+            const MiTokens tk = mi_tokens(first, tiles, a.E, u);
+            const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(((tk.cols + 15) & ~15) >> 3) << 17) |
+                                   ((uint32_t)(MI_BM >> 4) << 24);  // s32 += s8 x s8, both K-major
+            const uint32_t slot = tc % SLOTS;
+            if (tc >= SLOTS && !mi_wait_warp(mi_smem(&accempty[slot]), (tc / SLOTS - 1) & 1u, &s_abort, err)) break;
+            asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+            const uint32_t dst = tmem + slot * BN;
+            for (int kt = kt0; kt < kt1; kt++) {
+                if (!mi_wait_warp(full0 + 8 * s, ph, &s_abort, err)) {
+                    ok = false;
+                    break;
+                }
                 asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-                const uint32_t dst = tmem + slot * BN;
-                for (int kt = kt0; kt < kt1; kt++) {
-                    if (!mi_wait(mi_smem(&full[s]), ph, &s_abort, err)) {
-                        ok = false;
-                        break;
-                    }
-                    asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-                    const uint32_t wa = mi_smem(ring + s * STAGE), xa = wa + MI_W_BYTES;
+                if (lead) {
+                    const uint32_t wd = desc0 + s * (STAGE >> 4), xd = wd + (MI_W_BYTES >> 4);
 #pragma unroll
                     for (int kc = 0; kc < MI_BK / 32; kc++)
-                        mi_mma(dst, mi_desc(wa + kc * 32), mi_desc(xa + kc * 32), idesc, (kt > kt0 || kc > 0) ? 1u : 0u);
-                    mi_commit(mi_smem(&empty[s]));
-                    if (++s == S) s = 0, ph ^= 1;
+                        mi_mma(dst, wd + 2 * kc, xd + 2 * kc, idesc, (kt > kt0 || kc > 0) ? 1u : 0u);
+                    mi_commit(empty0 + 8 * s);
+                    if (kt == kt1 - 1) mi_commit(mi_smem(&accfull[slot]));
                 }
-                if (ok) mi_commit(mi_smem(&accfull[slot]));
-                u += du, m += dm;
-                if (m >= a.mt) m -= a.mt, u++;
+                if (++s == (uint32_t)S) s = 0, ph ^= 1;
             }
-            // every MMA issued is complete before the tensor memory is freed
+            u += du, m += dm;
+            if (m >= a.mt) m -= a.mt, u++;
+        }
+        // every MMA issued is complete before the tensor memory is freed
+        if (lead) {
             mi_commit(mi_smem(&fin));
             mi_drain(mi_smem(&fin), 0);
         }
@@ -557,7 +573,7 @@ int launch_mi(fp_ctx* c, MiArgs& a, int64_t tiles, int split, cudaStream_t st) {
     const size_t extra = (SPLIT ? (size_t)split * a.per * MI_BM * 4 : 0) + 8 * ((size_t)a.E + 1) + 1024;
     a.stages = (int)std::min<size_t>(MI_MAX_STAGES, (MI_SMEM - extra) / STAGE);
     auto kern = matmul_i8_kernel<BN, SPLIT, COPY>;
-    FP_CUDA(c, cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MI_SMEM));
+    FP_CUDA(c, fp_op_smem(c, 1 + (BN == 32 ? 0 : BN == 128 ? 4 : 8) + 2 * SPLIT + COPY, kern, MI_SMEM));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : std::min<int64_t>(tiles, c->num_sms)));
     cfg.blockDim = dim3(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS : 0));

@@ -117,20 +117,37 @@ __global__ void __launch_bounds__(1024)
 
 // ---- dispatch -------------------------------------------------------------------------------
 
-// rows[pos[t][j]] = x[t] in units of VT; one token per tpr threads, blockIdx.y a share of the columns
-template <typename VT>
+constexpr int MO_CHOICES = 4;  // positions (and weights) of a token kept in registers at a time
+
+// rows[pos[t][j]] = x[t] in units of VT; one token per tpr threads, blockIdx.y a share of the columns. U
+// loads of a thread are in flight before its stores.
+template <typename VT, int U>
 __global__ void __launch_bounds__(256)
     moe_dispatch_kernel(const char* __restrict__ x, int64_t T, int64_t nvec, int64_t ldx, const int32_t* __restrict__ pos,
                         int k, int64_t R, char* __restrict__ rows, int64_t ldr, int tpr) {
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
     const VT* src = reinterpret_cast<const VT*>(x + t * ldx);
-    const int64_t step = (int64_t)tpr * gridDim.y;
-    for (int64_t c = threadIdx.x % tpr + (int64_t)tpr * blockIdx.y; c < nvec; c += step) {
-        const VT v = src[c];
-        for (int j = 0; j < k; j++) {
-            const int64_t p = pos[t * k + j];
-            if (p >= 0 && p < R) reinterpret_cast<VT*>(rows + p * ldr)[c] = v;
+    const int64_t step = (int64_t)tpr * gridDim.y, c0 = threadIdx.x % tpr + (int64_t)tpr * blockIdx.y;
+    for (int j0 = 0; j0 < k; j0 += MO_CHOICES) {
+        VT* dst[MO_CHOICES];
+#pragma unroll
+        for (int j = 0; j < MO_CHOICES; j++) {
+            const int64_t p = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
+            dst[j] = p >= 0 && p < R ? reinterpret_cast<VT*>(rows + p * ldr) : nullptr;
+        }
+        for (int64_t c = c0; c < nvec; c += U * step) {
+            VT v[U];
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if (c + u * step < nvec) v[u] = src[c + u * step];
+#pragma unroll
+            for (int j = 0; j < MO_CHOICES; j++) {
+                if (!dst[j]) continue;
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    if (c + u * step < nvec) dst[j][c + u * step] = v[u];
+            }
         }
     }
 }
@@ -138,6 +155,7 @@ __global__ void __launch_bounds__(256)
 template <typename VT>
 void launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, int64_t ldx, const int32_t* pos, int k,
                      int64_t R, void* rows, int64_t ldr, cudaStream_t st) {
+    constexpr int U = sizeof(VT) == 16 ? 4 : 8;
     const int64_t nvec = bytes / (int64_t)sizeof(VT);
     int tpr = 32;
     while (tpr < 256 && tpr < nvec) tpr *= 2;
@@ -145,14 +163,15 @@ void launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, i
     const int64_t gx = (T + rpb - 1) / rpb;
     // few tokens: their columns over more blocks
     const int64_t gy = std::max<int64_t>(1, std::min((nvec + tpr - 1) / tpr, 4 * (int64_t)c->num_sms / gx));
-    moe_dispatch_kernel<VT><<<dim3((unsigned)gx, (unsigned)gy), 256, 0, st>>>((const char*)x, T, nvec, ldx, pos, k, R,
+    moe_dispatch_kernel<VT, U><<<dim3((unsigned)gx, (unsigned)gy), 256, 0, st>>>((const char*)x, T, nvec, ldx, pos, k, R,
                                                                              (char*)rows, ldr, tpr);
 }
 
 // ---- combine --------------------------------------------------------------------------------
 
-// out[t] = base[t] + sum_j w[t][j] rows[pos[t][j]] in fp32, rounded once; V elements per load
-template <typename RT, typename OT, int V>
+// out[t] = base[t] + sum_j w[t][j] rows[pos[t][j]] in fp32, rounded once; V elements per load, U vectors
+// of a thread at a time
+template <typename RT, typename OT, int V, int U>
 __global__ void __launch_bounds__(256)
     moe_combine_kernel(const RT* __restrict__ rows, int64_t R, int64_t ldr, const int32_t* __restrict__ pos,
                        const float* __restrict__ w, const OT* base, int64_t ldb, int64_t T, int k, int64_t M, OT* out,
@@ -160,74 +179,128 @@ __global__ void __launch_bounds__(256)
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
     const int64_t nvec = M / V, step = (int64_t)tpr * gridDim.y;
-    for (int64_t c = threadIdx.x % tpr + (int64_t)tpr * blockIdx.y; c < nvec; c += step) {
-        float acc[V];
-        if (base) {
-            const FpVec<OT, V> b = *reinterpret_cast<const FpVec<OT, V>*>(base + t * ldb + c * V);
+    const FpVec<RT, V>* src[MO_CHOICES];
+    float s[MO_CHOICES];
+    auto choices = [&](int j0) {
 #pragma unroll
-            for (int i = 0; i < V; i++) acc[i] = fp_to_f(b.v[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; i++) acc[i] = 0.0f;
+        for (int j = 0; j < MO_CHOICES; j++) {
+            const int64_t p = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
+            src[j] = p >= 0 && p < R ? reinterpret_cast<const FpVec<RT, V>*>(rows + p * ldr) : nullptr;
+            s[j] = w && j0 + j < k ? __ldg(w + t * k + j0 + j) : 1.0f;
         }
-        for (int j = 0; j < k; j++) {
-            const int64_t p = pos[t * k + j];
-            if (p < 0 || p >= R) continue;
-            const float s = w ? w[t * k + j] : 1.0f;
-            const FpVec<RT, V> v = *reinterpret_cast<const FpVec<RT, V>*>(rows + p * ldr + c * V);
+    };
+    choices(0);
+    for (int64_t c = threadIdx.x % tpr + (int64_t)tpr * blockIdx.y; c < nvec; c += U * step) {
+        float acc[U][V];
 #pragma unroll
-            for (int i = 0; i < V; i++) acc[i] = fmaf(s, fp_to_f(v.v[i]), acc[i]);
+        for (int u = 0; u < U; u++) {
+            FpVec<OT, V> b;
+            const bool in = base && c + u * step < nvec;
+            if (in) b = *reinterpret_cast<const FpVec<OT, V>*>(base + t * ldb + (c + u * step) * V);
+#pragma unroll
+            for (int i = 0; i < V; i++) acc[u][i] = in ? fp_to_f(b.v[i]) : 0.0f;
         }
-        FpVec<OT, V> o;
+        for (int j0 = 0; j0 < k; j0 += MO_CHOICES) {
+            if (k > MO_CHOICES) choices(j0);
+            // the loads of two choices at a time, then their sums in the order of the choices
 #pragma unroll
-        for (int i = 0; i < V; i++) o.v[i] = fp_from_f<OT>(acc[i]);
-        *reinterpret_cast<FpVec<OT, V>*>(out + t * ldo + c * V) = o;
+            for (int jj = 0; jj < MO_CHOICES; jj += 2) {
+                if (j0 + jj >= k) break;
+                FpVec<RT, V> v[2][U];
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+#pragma unroll
+                    for (int u = 0; u < U; u++)
+                        if (src[jj + j] && c + u * step < nvec) v[j][u] = src[jj + j][c + u * step];
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    if (!src[jj + j]) continue;
+#pragma unroll
+                    for (int u = 0; u < U; u++)
+#pragma unroll
+                        for (int i = 0; i < V; i++) acc[u][i] = fmaf(s[jj + j], fp_to_f(v[j][u].v[i]), acc[u][i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (c + u * step >= nvec) break;
+            FpVec<OT, V> o;
+#pragma unroll
+            for (int i = 0; i < V; i++) o.v[i] = fp_from_f<OT>(acc[u][i]);
+            *reinterpret_cast<FpVec<OT, V>*>(out + t * ldo + (c + u * step) * V) = o;
+        }
     }
 }
 
 // ---- gradients of combine -------------------------------------------------------------------
 
 // One token per block: its k rows' gradients and the k inner products (fp32, a fixed order: a thread's
-// columns, then the block's tree)
-template <typename RT, typename OT, int V>
+// columns, then the block's tree). Two choices at a time read dout once.
+template <typename RT, typename OT, int V, int U>
 __global__ void __launch_bounds__(256)
     moe_grad_kernel(const OT* __restrict__ dout, int64_t ldd, const RT* __restrict__ rows, int64_t R, int64_t ldr,
                     const int32_t* __restrict__ pos, const float* __restrict__ w, int64_t T, int k, int64_t M,
                     RT* __restrict__ drows, int64_t lddr, float* __restrict__ dw) {
-    __shared__ float red[8];
-    const int64_t t = blockIdx.x, nvec = M / V;
+    __shared__ float red[2][8];
+    const int64_t t = blockIdx.x, nvec = M / V, step = blockDim.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int j = 0; j < k; j++) {
-        const int64_t p = pos[t * k + j];
-        const bool ok = p >= 0 && p < R;
-        float dot = 0.0f;
-        if (ok) {
-            const float s = w ? w[t * k + j] : 1.0f;
-            for (int64_t c = threadIdx.x; c < nvec; c += blockDim.x) {
-                const FpVec<OT, V> g = *reinterpret_cast<const FpVec<OT, V>*>(dout + t * ldd + c * V);
-                if (dw) {
-                    const FpVec<RT, V> v = *reinterpret_cast<const FpVec<RT, V>*>(rows + p * ldr + c * V);
+    const FpVec<OT, V>* g = reinterpret_cast<const FpVec<OT, V>*>(dout + t * ldd);
+    for (int j0 = 0; j0 < k; j0 += 2) {
+        int64_t p[2];
+        float s[2], dot[2] = {0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < V; i++) dot = fmaf(fp_to_f(g.v[i]), fp_to_f(v.v[i]), dot);
-                }
-                if (drows) {
-                    FpVec<RT, V> o;
+        for (int j = 0; j < 2; j++) {
+            p[j] = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
+            if (p[j] >= R) p[j] = -1;
+            s[j] = w && j0 + j < k ? __ldg(w + t * k + j0 + j) : 1.0f;
+        }
+        for (int64_t c = threadIdx.x; c < nvec && (p[0] >= 0 || p[1] >= 0); c += U * step) {
+            FpVec<OT, V> gv[U];
+            FpVec<RT, V> v[2][U];
 #pragma unroll
-                    for (int i = 0; i < V; i++) o.v[i] = fp_from_f<RT>(s * fp_to_f(g.v[i]));
-                    *reinterpret_cast<FpVec<RT, V>*>(drows + p * lddr + c * V) = o;
+            for (int u = 0; u < U; u++)
+                if (c + u * step < nvec) gv[u] = g[c + u * step];
+            if (dw) {
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+#pragma unroll
+                    for (int u = 0; u < U; u++)
+                        if (p[j] >= 0 && c + u * step < nvec)
+                            v[j][u] = reinterpret_cast<const FpVec<RT, V>*>(rows + p[j] * ldr)[c + u * step];
+            }
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                if (p[j] < 0) continue;
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    if (c + u * step >= nvec) break;
+                    if (dw) {
+#pragma unroll
+                        for (int i = 0; i < V; i++) dot[j] = fmaf(fp_to_f(gv[u].v[i]), fp_to_f(v[j][u].v[i]), dot[j]);
+                    }
+                    if (drows) {
+                        FpVec<RT, V> o;
+#pragma unroll
+                        for (int i = 0; i < V; i++) o.v[i] = fp_from_f<RT>(s[j] * fp_to_f(gv[u].v[i]));
+                        reinterpret_cast<FpVec<RT, V>*>(drows + p[j] * lddr)[c + u * step] = o;
+                    }
                 }
             }
         }
         if (dw) {
+            if (j0) __syncthreads();  // red may still be read for the choices before
 #pragma unroll
-            for (int m = 16; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-            __syncthreads();  // red may still be read for the choice before
-            if (lane == 0) red[warp] = dot;
+            for (int j = 0; j < 2; j++) {
+#pragma unroll
+                for (int m = 16; m > 0; m >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], m);
+                if (lane == 0) red[j][warp] = dot[j];
+            }
             __syncthreads();
-            if (threadIdx.x == 0) {
+            if (threadIdx.x < 2 && j0 + (int)threadIdx.x < k) {
                 float a = 0.0f;
-                for (int i = 0; i < (int)(blockDim.x >> 5); i++) a += red[i];
-                dw[t * k + j] = ok ? a : 0.0f;
+                for (int i = 0; i < (int)(blockDim.x >> 5); i++) a += red[threadIdx.x][i];
+                dw[t * k + j0 + threadIdx.x] = a;  // 0 where there is no row: nothing was added
             }
         }
     }
@@ -271,7 +344,7 @@ int fp_moe_sort(fp_ctx* c, const int32_t* e, int64_t n, int E, int32_t* offsets,
     const int warps = (int)std::min<int64_t>(most, (need + blocks - 1) / blocks);
     const int threads = std::max(32 * warps, 128);
     const size_t smem = sizeof(int32_t) * ((size_t)warps * E + 2 * (size_t)E);
-    FP_CUDA(c, cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MS_HIST_BYTES + 8 * 4096));
+    FP_CUDA(c, fp_op_smem(c, 0, moe_sort_kernel, MS_HIST_BYTES + 8 * 4096));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3((unsigned)threads);
@@ -366,10 +439,10 @@ int fp_moe_combine(fp_ctx* c, const void* rows, int rows_type, int64_t R, int64_
             const int64_t gy = std::max<int64_t>(1, std::min((nvec + tpr - 1) / tpr, 4 * (int64_t)c->num_sms / gx));
             const dim3 grid((unsigned)gx, (unsigned)gy);
             if (vec)
-                moe_combine_kernel<RT, OT, V><<<grid, 256, 0, st>>>((const RT*)rows, R, ldr, pos, weights,
+                moe_combine_kernel<RT, OT, V, 2><<<grid, 256, 0, st>>>((const RT*)rows, R, ldr, pos, weights,
                                                                     (const OT*)base, ldb, T, k, M, (OT*)out, ldo, tpr);
             else
-                moe_combine_kernel<RT, OT, 1><<<grid, 256, 0, st>>>((const RT*)rows, R, ldr, pos, weights,
+                moe_combine_kernel<RT, OT, 1, 8><<<grid, 256, 0, st>>>((const RT*)rows, R, ldr, pos, weights,
                                                                     (const OT*)base, ldb, T, k, M, (OT*)out, ldo, tpr);
         });
     });
@@ -416,10 +489,10 @@ int fp_moe_combine_grad(fp_ctx* c, const void* dout, int out_type, int64_t ldd, 
                                               (uint64_t)lddr * rs}) == 16 &&
                              fp_common_align({(uint64_t)(uintptr_t)dout, (uint64_t)ldd * os}) >= OA;
             if (vec)
-                moe_grad_kernel<RT, OT, V><<<(unsigned)T, 256, 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos,
+                moe_grad_kernel<RT, OT, V, 2><<<(unsigned)T, 256, 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos,
                                                                         weights, T, k, M, (RT*)drows, lddr, dweights);
             else
-                moe_grad_kernel<RT, OT, 1><<<(unsigned)T, 256, 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos,
+                moe_grad_kernel<RT, OT, 1, 8><<<(unsigned)T, 256, 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos,
                                                                         weights, T, k, M, (RT*)drows, lddr, dweights);
         });
     });

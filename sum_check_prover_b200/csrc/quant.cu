@@ -15,19 +15,35 @@ namespace {
 
 constexpr int QR_VALUES = 32;  // values of a row that a thread keeps in registers
 
-// n + 1, n or the even one of them, as |x| 127 / a lies above, below or at n + 1/2
-__device__ __noinline__ int quant_near_half(float ax, float a, float t) {
-    const int n = (int)floorf(t);
-    const double d = 254.0 * (double)ax - (double)(2 * n + 1) * (double)a;
-    return d > 0 ? n + 1 : d < 0 ? n : n + (n & 1);
+constexpr float QR_MAGIC = 12582912.0f;  // 1.5 * 2^23: t + it has the nearest integer to t in its low bits
+
+// the integer nearest to 127 x / a for a value that lies next to a half (t: the approximate quotient)
+__device__ __noinline__ uint32_t quant_near_half(float x, float a, float t) {
+    const int n = (int)floorf(fabsf(t));
+    const double d = 254.0 * (double)fabsf(x) - (double)(2 * n + 1) * (double)a;
+    const int r = d > 0 ? n + 1 : d < 0 ? n : n + (n & 1);
+    return (uint32_t)(x < 0 ? -r : r);
 }
 
-__device__ __forceinline__ int quant_one(float x, float a, float inv) {
-    const float ax = fabsf(x), t = ax * inv;
-    const float f = t - floorf(t);
-    int n = __float2int_rn(t);
-    if (fabsf(f - 0.5f) < 6.1035156e-5f) n = quant_near_half(ax, a, t);
-    return x < 0 ? -n : n;
+// V values to int8
+template <typename T, int V>
+__device__ __forceinline__ FpVec<int8_t, V> quant_vec(const FpVec<T, V>& w, float up, float a, float inv) {
+    FpVec<int8_t, V> o;
+    bool near = false;
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        const float t = fp_to_f(w.v[e]) * up * inv, r = t + QR_MAGIC;
+        o.v[e] = (int8_t)__float_as_uint(r);
+        near |= fabsf(t - (r - QR_MAGIC)) > 0.5f - 6.1035156e-5f;
+    }
+    if (near) {
+#pragma unroll
+        for (int e = 0; e < V; e++) {
+            const float x = fp_to_f(w.v[e]) * up, t = x * inv;
+            if (fabsf(t - (t + QR_MAGIC - QR_MAGIC)) > 0.5f - 6.1035156e-5f) o.v[e] = (int8_t)quant_near_half(x, a, t);
+        }
+    }
+    return o;
 }
 
 // One row per `tpr` threads (a multiple of 32 that divides the block). V: elements per load; a thread
@@ -86,9 +102,8 @@ __global__ void __launch_bounds__(1024)
         }
     }
     auto put = [&](int64_t c, const FpVec<T, V>& w) {
-        FpVec<int8_t, V> o;
-#pragma unroll
-        for (int e = 0; e < V; e++) o.v[e] = (inv == 0.0f) ? 0 : (int8_t)quant_one(fp_to_f(w.v[e]) * up, a, inv);
+        FpVec<int8_t, V> o = {};
+        if (inv != 0.0f) o = quant_vec<T, V>(w, up, a, inv);
         for (int j = 0; j < copies; j++) {
             const int64_t p = pos ? pos[row * k + j] : row;
             if (p < 0 || p >= R) continue;

@@ -39,11 +39,11 @@ class T:
             n *= s
         self._dense, self._stride, self._n = tuple(dense), tuple(stride or dense), n
 
-    def dim(self):
-        return len(self.shape)
+    def get_device(self):
+        return self.device.index
 
-    def stride(self, i):
-        return self._stride[i]
+    def stride(self):
+        return self._stride
 
     def is_contiguous(self):
         return all(s == d for s, d, n in zip(self._stride, self._dense, self.shape) if n > 1)
