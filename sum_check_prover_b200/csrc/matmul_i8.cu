@@ -127,20 +127,52 @@ __device__ __forceinline__ void mi_drain(uint32_t bar, uint32_t parity) { mi_wai
 __device__ __forceinline__ void mi_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
+// arrives when the MMAs issued so far are complete; PAIR: at the barrier of that offset in both blocks
+template <bool PAIR>
 __device__ __forceinline__ void mi_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+    if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+// an arrival at the barrier of that offset in block `rank` of the cluster
+__device__ __forceinline__ void mi_arrive_at(uint32_t bar, uint32_t rank) {
+    uint32_t there;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(bar), "r"(rank));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(there) : "memory");
 }
 // a, b: the low words of the operands' descriptors
+template <bool PAIR>
 __device__ __forceinline__ void mi_mma(uint32_t tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-        "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], da, db, %3, p;\n\t}\n" ::"r"(tmem),
-        "r"(a), "r"(b), "r"(idesc), "r"(MI_DESC_HI), "r"(add)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+            "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::2.kind::i8 [%0], da, db, %3, p;\n\t}\n" ::"r"(tmem),
+            "r"(a), "r"(b), "r"(idesc), "r"(MI_DESC_HI), "r"(add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+            "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::i8 [%0], da, db, %3, p;\n\t}\n" ::"r"(tmem),
+            "r"(a), "r"(b), "r"(idesc), "r"(MI_DESC_HI), "r"(add)
+            : "memory");
 }
+// PAIR: bar may be the other block's (an address in the cluster's window)
+template <bool PAIR>
 __device__ __forceinline__ void mi_tma(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
-    asm volatile(
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+            "[%1, {%2, %3}], [%4];\n" ::"r"(dst),
+            "l"(tm), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
         "[%4];\n" ::"r"(dst),
         "l"(tm), "r"(x), "r"(y), "r"(bar)
@@ -228,6 +260,12 @@ __device__ __forceinline__ MiTokens mi_tokens(const int32_t* first, const int32_
     return MiTokens{lo, first[lo] + at, min(width, n - at)};
 }
 
+// the columns of a tile's MMAs: kind::i8 takes multiples of 16 with 128 rows, of 32 with a pair's 256
+template <bool PAIR>
+__device__ __forceinline__ int mi_columns(int cols) {
+    return PAIR ? (cols + 31) & ~31 : (cols + 15) & ~15;
+}
+
 // y of 16 columns (tokens n .. n + cols - 1) for one channel
 template <typename YT>
 __device__ __forceinline__ void mi_store16(const MiArgs& a, const int32_t (&v)[16], int64_t n, int cols, int64_t m,
@@ -242,11 +280,13 @@ __device__ __forceinline__ void mi_store16(const MiArgs& a, const int32_t (&v)[1
     }
 }
 
-template <int BN, bool SPLIT, bool COPY>
+template <int BN, bool SPLIT, bool COPY, bool PAIR>
 __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS : 0), 1)
     matmul_i8_kernel(const __grid_constant__ MiArgs a) {
-    constexpr int XB = mi_box_rows(BN);
-    constexpr int STAGE = MI_W_BYTES + BN * MI_BK;
+    static_assert(!(PAIR && (SPLIT || COPY)), "a pair has one tile at a time and TMA operands");
+    constexpr int XB = mi_box_rows(BN), XROWS = PAIR ? BN / 2 : BN;  // token rows of a box, of this block's stage
+    constexpr int STAGE = MI_W_BYTES + XROWS * MI_BK;
+    constexpr int TM = PAIR ? 2 * MI_BM : MI_BM;  // channels of a tile
     constexpr int SLOTS = SPLIT ? 1 : 2;
     constexpr int TCOLS = SLOTS * BN;
     extern __shared__ uint8_t mi_raw[];
@@ -260,7 +300,7 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nthr = blockDim.x;
     const int S = a.stages;
     uint32_t crank = 0, csize = 1;
-    if (SPLIT) {
+    if (SPLIT || PAIR) {
         asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
         asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
     }
@@ -275,7 +315,7 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
         }
         for (int s = 0; s < 2; s++) {
             mi_bar_init(&accfull[s], 1);
-            mi_bar_init(&accempty[s], 128);
+            mi_bar_init(&accempty[s], PAIR ? 8 : 4);  // a warp of the epilogue each
         }
         mi_bar_init(&fin, 1);
         mi_bar_init(&redfull, SPLIT ? max(1, 4 * ((int)csize - 1)) : 1);
@@ -283,10 +323,17 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(mi_smem(&tmem_base)),
-                     "n"(TCOLS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(mi_smem(&tmem_base)),
+                         "n"(TCOLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(mi_smem(&tmem_base)),
+                         "n"(TCOLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+        }
     }
     // the experts' first rows (each offset counted as the largest up to it, inside [0, N]) and the prefix
     // sums of their token tiles
@@ -340,44 +387,53 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
     asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-    if (SPLIT) {  // the other blocks' barriers are there before anything arrives at them
+    if (SPLIT || PAIR) {  // the other blocks' barriers are there before anything arrives at them
         asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;\n" ::: "memory");
     }
     const uint32_t tmem = tmem_base;
     const int total_u = tiles[a.E];  // token tiles; tile (u, m) of channel tile m
-    // this block's (SPLIT: this cluster's) first tile and its step; SPLIT has one tile per cluster
-    const int walkers = SPLIT ? 0x7fffffff : (int)gridDim.x;
-    const int start = SPLIT ? (int)(blockIdx.x / csize) : (int)blockIdx.x;
-    const int u0 = start / a.mt, mm0 = start % a.mt, du = SPLIT ? 0x3fffffff : walkers / a.mt, dm = SPLIT ? 0 : walkers % a.mt;
+    // this block's (SPLIT, PAIR: this cluster's) first tile and its step; SPLIT has one tile per cluster
+    const int start = (int)(blockIdx.x / csize), walkers = (int)(gridDim.x / csize);
+    const int u0 = start / a.mt, mm0 = start % a.mt;
+    const int du = SPLIT ? 0x3fffffff : walkers / a.mt, dm = SPLIT ? 0 : walkers % a.mt;
     const int kt0 = SPLIT ? (int)((int64_t)a.nk * crank / csize) : 0;
     const int kt1 = SPLIT ? (int)((int64_t)a.nk * (crank + 1) / csize) : a.nk;
+    const int wlead = PAIR ? (int)crank * MI_BM : 0;  // this block's channels of a tile
     volatile uint64_t* err = a.err;
 
     if (warp == 0) {
         // ---- TMA: the whole warp walks and waits, one lane issues ----
         const bool lead = mi_elect();
         const uint32_t full0 = mi_smem(full), empty0 = mi_smem(empty), ring0 = mi_smem(ring);
+        uint32_t fulls = full0;  // where the copies are counted: PAIR, the first block's barriers
+        if (PAIR) asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(fulls) : "r"(full0));
         uint32_t s = 0, ph = 1;  // a fresh barrier's "previous phase" counts as complete
         uint32_t issued = 0;
         bool ok = true;
         for (int u = u0, m = mm0; u < total_u && ok;) {
             const MiTokens tk = mi_tokens(first, tiles, a.E, u);
-            const int boxes = (tk.cols + XB - 1) / XB;
+            // PAIR: half of the MMA's columns each, and both blocks' bytes awaited by the issuing block
+            const int half = PAIR ? mi_columns<PAIR>(tk.cols) >> 1 : 0;
+            const int boxes = ((PAIR ? half : tk.cols) + XB - 1) / XB, xrow = tk.n0 + (PAIR ? (int)crank * half : 0);
             const uint32_t bytes = (COPY && a.copy_w ? 0 : MI_W_BYTES) + (COPY && a.copy_x ? 0 : boxes * XB * MI_BK);
-            const int wrow = tk.e * a.M + m * MI_BM;
+            const int wrow = tk.e * a.M + m * TM + wlead;
             for (int kt = kt0; kt < kt1; kt++) {
                 if (!mi_wait_warp(empty0 + 8 * s, ph, &s_abort, err)) {
                     ok = false;
                     break;
                 }
                 if (lead) {
-                    const uint32_t fb = full0 + 8 * s, dst = ring0 + s * STAGE;
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(fb), "r"(bytes) : "memory");
-                    if (!COPY || !a.copy_w) mi_tma(dst, &a.tw, kt * MI_BK, wrow, fb);
+                    const uint32_t fb = fulls + 8 * s, dst = ring0 + s * STAGE;
+                    if (!PAIR || crank == 0)
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(full0 + 8 * s),
+                                     "r"(PAIR ? 2 * bytes : bytes)
+                                     : "memory");
+                    if (!COPY || !a.copy_w) mi_tma<PAIR>(dst, &a.tw, kt * MI_BK, wrow, fb);
                     if (!COPY || !a.copy_x) {
 #pragma unroll
-                        for (int b = 0; b < BN / XB; b++)
-                            if (b < boxes) mi_tma(dst + MI_W_BYTES + b * XB * MI_BK, &a.tx, kt * MI_BK, tk.n0 + b * XB, fb);
+                        for (int b = 0; b < XROWS / XB; b++)
+                            if (b < boxes)
+                                mi_tma<PAIR>(dst + MI_W_BYTES + b * XB * MI_BK, &a.tx, kt * MI_BK, xrow + b * XB, fb);
                     }
                 }
                 issued++;
@@ -387,28 +443,30 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
             if (m >= a.mt) m -= a.mt, u++;
         }
         if (!ok && lead) {
-            if (!COPY) {
+            if (!COPY && !PAIR) {
                 // every copy that was issued lands before the block ends
                 for (uint32_t i = issued > (uint32_t)S ? issued - S : 0; i < issued; i++)
                     mi_drain(full0 + 8 * (i % S), (i / S) & 1u);
             } else {
-                // (the copying warps' arrivals may be missing: the phases never complete, time has to do)
+                // (other warps' arrivals may be missing, so that the phases never complete: time has to do)
                 for (int i = 0; i < 64; i++) __nanosleep(1000000);
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ---- MMA issue: the same way ----
+    } else if (warp == 1 && (!PAIR || crank == 0)) {
+        // ---- MMA issue: the same way; PAIR: for both blocks ----
         const bool lead = mi_elect();
         const uint32_t full0 = mi_smem(full), empty0 = mi_smem(empty), desc0 = mi_desc_lo(mi_smem(ring));
         uint32_t s = 0, ph = 0, tc = 0;
         bool ok = true;
         for (int u = u0, m = mm0; u < total_u && ok; tc++) {
             const MiTokens tk = mi_tokens(first, tiles, a.E, u);
-            const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(((tk.cols + 15) & ~15) >> 3) << 17) |
-                                   ((uint32_t)(MI_BM >> 4) << 24);  // s32 += s8 x s8, both K-major
+            const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(mi_columns<PAIR>(tk.cols) >> 3) << 17) |
+                                   ((uint32_t)(TM >> 4) << 24);  // s32 += s8 x s8, both K-major
             const uint32_t slot = tc % SLOTS;
-            if (tc >= SLOTS && !mi_wait_warp(mi_smem(&accempty[slot]), (tc / SLOTS - 1) & 1u, &s_abort, err)) break;
+            if (tc >= SLOTS && !__all_sync(0xffffffffu, mi_wait_scope<PAIR>(mi_smem(&accempty[slot]), (tc / SLOTS - 1) & 1u,
+                                                                        &s_abort, err)))
+                break;
             asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
             const uint32_t dst = tmem + slot * BN;
             for (int kt = kt0; kt < kt1; kt++) {
@@ -421,9 +479,9 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
                     const uint32_t wd = desc0 + s * (STAGE >> 4), xd = wd + (MI_W_BYTES >> 4);
 #pragma unroll
                     for (int kc = 0; kc < MI_BK / 32; kc++)
-                        mi_mma(dst, wd + 2 * kc, xd + 2 * kc, idesc, (kt > kt0 || kc > 0) ? 1u : 0u);
-                    mi_commit(empty0 + 8 * s);
-                    if (kt == kt1 - 1) mi_commit(mi_smem(&accfull[slot]));
+                        mi_mma<PAIR>(dst, wd + 2 * kc, xd + 2 * kc, idesc, (kt > kt0 || kc > 0) ? 1u : 0u);
+                    mi_commit<PAIR>(empty0 + 8 * s);
+                    if (kt == kt1 - 1) mi_commit<PAIR>(mi_smem(&accfull[slot]));
                 }
                 if (++s == (uint32_t)S) s = 0, ph ^= 1;
             }
@@ -432,18 +490,18 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
         }
         // every MMA issued is complete before the tensor memory is freed
         if (lead) {
-            mi_commit(mi_smem(&fin));
+            mi_commit<PAIR>(mi_smem(&fin));
             mi_drain(mi_smem(&fin), 0);
         }
         __syncwarp();
-    } else if (warp < 6) {
+    } else if (warp >= 2 && warp < 6) {
         // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31 ----
         const int qd = warp & 3;
         uint32_t tc = 0;
         for (int u = u0, m = mm0; u < total_u; tc++) {
             const MiTokens tk = mi_tokens(first, tiles, a.E, u);
             const uint32_t slot = tc % SLOTS;
-            const int64_t row = (int64_t)m * MI_BM + 32 * qd + lane;
+            const int64_t row = (int64_t)m * TM + wlead + 32 * qd + lane;
             const bool live = row < a.M;
             const float ws = live ? __ldg(a.w_scale + (int64_t)tk.e * a.M + row) : 0.0f;
             if (!mi_wait_warp(mi_smem(&accfull[slot]), (tc / SLOTS) & 1u, &s_abort, err)) break;
@@ -488,10 +546,7 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
                 __syncwarp();
                 if (lane == 0) {
                     for (uint32_t d = 0; d < csize; d++) {
-                        if (d == crank) continue;
-                        uint32_t bar;
-                        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(mi_smem(&redfull)), "r"(d));
-                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+                        if (d != crank) mi_arrive_at(mi_smem(&redfull), d);
                     }
                 }
                 __syncwarp();
@@ -521,11 +576,17 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
-            mi_arrive(mi_smem(&accempty[slot]));
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR)
+                    mi_arrive_at(mi_smem(&accempty[slot]), 0);
+                else
+                    mi_arrive(mi_smem(&accempty[slot]));
+            }
             u += du, m += dm;
             if (m >= a.mt) m -= a.mt, u++;
         }
-    } else if (COPY) {
+    } else if (COPY && warp >= 6) {
         // ---- operands that TMA cannot read: group g of four warps fills every MI_COPY_GROUPS-th k-tile ----
         const int g = (warp - 6) >> 2, t = tid - MI_BASE_THREADS - 128 * g;
         int s = 0, turn = 0;
@@ -533,7 +594,7 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
         bool ok = true;
         for (int u = u0, m = mm0; u < total_u && ok;) {
             const MiTokens tk = mi_tokens(first, tiles, a.E, u);
-            const int rows16 = (tk.cols + 15) & ~15;
+            const int rows16 = mi_columns<false>(tk.cols);
             for (int kt = kt0; kt < kt1; kt++) {
                 if (turn == g) {
                     if (!mi_wait_warp(mi_smem(&empty[s]), ph, &s_abort, err)) {
@@ -561,53 +622,75 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
     asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-    if (SPLIT)  // no block leaves while another may still write to it
+    if (SPLIT || PAIR)  // no block leaves while another may still write to it or read its operands
         asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;\n" ::: "memory");
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "n"(TCOLS));
+    if (warp == 1) {
+        if (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "n"(TCOLS));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "n"(TCOLS));
+    }
 }
 
-template <int BN, bool SPLIT, bool COPY>
-int launch_mi(fp_ctx* c, MiArgs& a, int64_t tiles, int split, cudaStream_t st) {
-    constexpr int STAGE = MI_W_BYTES + BN * MI_BK;
+template <int BN, bool SPLIT, bool COPY, bool PAIR>
+int launch_mi(fp_ctx* c, MiArgs& a, int64_t token_tiles, int split, cudaStream_t st) {
+    constexpr int STAGE = MI_W_BYTES + (PAIR ? BN / 2 : BN) * MI_BK;
+    constexpr int TM = PAIR ? 2 * MI_BM : MI_BM;
+    const int cluster = PAIR ? 2 : split;
+    a.mt = (a.M + TM - 1) / TM;
     a.per = SPLIT ? (((BN + split - 1) / split) + 7) & ~7 : 0;
     const size_t extra = (SPLIT ? (size_t)split * a.per * MI_BM * 4 : 0) + 8 * ((size_t)a.E + 1) + 1024;
     a.stages = (int)std::min<size_t>(MI_MAX_STAGES, (MI_SMEM - extra) / STAGE);
-    auto kern = matmul_i8_kernel<BN, SPLIT, COPY>;
-    FP_CUDA(c, fp_op_smem(c, 1 + (BN == 32 ? 0 : BN == 128 ? 4 : 8) + 2 * SPLIT + COPY, kern, MI_SMEM));
+    auto kern = matmul_i8_kernel<BN, SPLIT, COPY, PAIR>;
+    FP_CUDA(c, fp_op_smem(c, 1 + (BN == 32 ? 0 : BN == 128 ? 8 : 16) + 4 * SPLIT + 2 * COPY + PAIR, kern, MI_SMEM));
+    const int64_t tiles = token_tiles * a.mt;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * split : std::min<int64_t>(tiles, c->num_sms)));
+    cfg.gridDim = dim3((unsigned)(cluster * (SPLIT ? tiles : std::min<int64_t>(tiles, c->num_sms / cluster))));
     cfg.blockDim = dim3(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS : 0));
     cfg.dynamicSmemBytes = a.stages * STAGE + extra;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)split;
+    at[0].val.clusterDim.x = (unsigned)cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = SPLIT ? 1 : 0;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
     FP_CUDA(c, cudaLaunchKernelEx(&cfg, kern, a));
     return FP_OK;
 }
 
-// BN by the tokens that a group has, the split by the tiles there are
-template <int BN>
-int launch_bn(fp_ctx* c, MiArgs& a, cudaStream_t st) {
-    // operands whose rows TMA can address; the others are copied by warps
+// operands whose rows TMA can address (the others are copied by warps); true if both are
+bool mi_maps(MiArgs& a, int bn) {
     a.copy_w = ((uintptr_t)a.w | (uint64_t)a.ldw) % 16 != 0 ||
                !fp_tmap_u8_2d(&a.tw, a.w, (uint64_t)a.K, (uint64_t)a.E * a.M, (uint64_t)a.ldw, MI_BK, MI_BM, true);
     a.copy_x = ((uintptr_t)a.x | (uint64_t)a.ldx) % 16 != 0 ||
-               !fp_tmap_u8_2d(&a.tx, a.x, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.ldx, MI_BK, mi_box_rows(BN), true);
-    const bool copy = a.copy_w || a.copy_x;
-    // tiles at most: every group that can have rows has one token tile, and the rows fill the others
+               !fp_tmap_u8_2d(&a.tx, a.x, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.ldx, MI_BK, mi_box_rows(bn), true);
+    return !a.copy_w && !a.copy_x;
+}
+
+// token tiles at most: every group that can have rows has one, and the rows fill the others
+int64_t mi_token_tiles(const MiArgs& a, int bn) {
     const int64_t groups = std::min(a.E, a.N);
-    const int64_t tiles = a.mt * (groups == 1 ? (a.N + BN - 1) / BN : groups + a.N / BN);
-    if constexpr (BN <= 128) {
-        int split = 1;
-        while (split < 8 && tiles * split * 2 <= c->num_sms && split * 4 <= a.nk) split *= 2;
-        if (split > 1)
-            return copy ? launch_mi<BN, true, true>(c, a, tiles, split, st) : launch_mi<BN, true, false>(c, a, tiles, split, st);
+    return groups == 1 ? (a.N + bn - 1) / bn : groups + a.N / bn;
+}
+
+int launch_split_or_not(fp_ctx* c, MiArgs& a, int64_t rows, cudaStream_t st) {
+    // a group of more than 32 rows fills wider tiles
+    const int bn = rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+    const int64_t tiles = mi_token_tiles(a, bn) * ((a.M + MI_BM - 1) / MI_BM);
+    const bool tma = mi_maps(a, bn);
+    int split = 1;
+    while (bn <= 128 && split < 8 && tiles * split * 2 <= c->num_sms && split * 4 <= a.nk) split *= 2;
+    const int64_t tt = mi_token_tiles(a, bn);
+    if (bn == 32) {
+        if (split > 1) return tma ? launch_mi<32, true, false, false>(c, a, tt, split, st) : launch_mi<32, true, true, false>(c, a, tt, split, st);
+        return tma ? launch_mi<32, false, false, false>(c, a, tt, 1, st) : launch_mi<32, false, true, false>(c, a, tt, 1, st);
     }
-    return copy ? launch_mi<BN, false, true>(c, a, tiles, 1, st) : launch_mi<BN, false, false>(c, a, tiles, 1, st);
+    if (split > 1) return tma ? launch_mi<128, true, false, false>(c, a, tt, split, st) : launch_mi<128, true, true, false>(c, a, tt, split, st);
+    // wider tiles: pairs of blocks, or one block that copies
+    const int64_t wide = mi_token_tiles(a, 256);
+    if (mi_maps(a, 256)) return launch_mi<256, false, false, true>(c, a, wide, 1, st);
+    return launch_mi<256, false, true, false>(c, a, wide, 1, st);
 }
 
 }  // namespace
@@ -643,14 +726,13 @@ int fp_matmul_i8(fp_ctx* c, const int8_t* w, int64_t ldw, const float* w_scale, 
     a.w = w, a.w_scale = w_scale, a.x = x, a.x_scale = x_scale, a.offsets = offsets, a.y = y;
     a.ldw = ldw, a.ldx = ldx, a.ldy = ldy;
     a.M = (int32_t)M, a.K = (int32_t)K, a.N = (int32_t)N, a.E = E, a.y_type = y_type;
-    a.mt = (int32_t)((M + MI_BM - 1) / MI_BM);
     a.nk = (int32_t)((K + MI_BK - 1) / MI_BK);
     a.err = &c->mb_dev->op_err;
     // rows of a group: N of a dense product, twice the mean of those that can have rows by expert
     const int64_t rows = E == 1 ? N : 2 * ((N + std::min<int64_t>(E, N) - 1) / std::min<int64_t>(E, N));
     int slot;
     fp_op_tic(c, st, K_MATMUL_I8, (double)std::min<int64_t>(E, N) * M * K + (double)N * (K + ys * (double)M), &slot);
-    const int rc = rows <= 32 ? launch_bn<32>(c, a, st) : rows <= 128 ? launch_bn<128>(c, a, st) : launch_bn<256>(c, a, st);
+    const int rc = launch_split_or_not(c, a, rows, st);
     fp_toc(c, st, slot);
     return rc;
 }
