@@ -32,6 +32,8 @@ namespace {
 constexpr int MS_HIST_BYTES = 176 * 1024;
 constexpr int MS_MAX_CLUSTER = 8;
 
+constexpr int MS_KEEP = 8;  // choices of a lane that stay in registers between the passes
+
 __global__ void __launch_bounds__(1024)
     moe_sort_kernel(const int32_t* __restrict__ e, int64_t n, int E, int warps, int32_t* __restrict__ offsets,
                     int32_t* __restrict__ pos) {
@@ -44,24 +46,38 @@ __global__ void __launch_bounds__(1024)
     __shared__ int32_t wsum[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nthr = blockDim.x;
 
-    for (int i = tid; i < warps * E; i += nthr) hist[i] = 0;
-    __syncthreads();
     // this warp's run of choices, a multiple of 32
     const int64_t run = ((n + (int64_t)C * warps - 1) / ((int64_t)C * warps) + 31) / 32 * 32;
-    const int64_t lo = min(n, ((int64_t)rank * warps + warp) * run), hi = min(n, lo + run);
+    const int64_t lo = warp < warps ? min(n, ((int64_t)rank * warps + warp) * run) : n, hi = min(n, lo + run);
+    const bool kept = run <= 32 * MS_KEEP;
+    int32_t keep[MS_KEEP];  // -1: none
+    auto fetch = [&](int64_t i) {
+#pragma unroll
+        for (int v = 0; v < MS_KEEP; v++) {
+            const int64_t at = i + 32 * v + lane;
+            keep[v] = at < hi ? __ldg(e + at) : -1;
+            if (keep[v] >= E) keep[v] = -1;
+        }
+    };
+    if (kept) fetch(lo);
+    for (int i = tid; i < warps * E; i += nthr) hist[i] = 0;
+    __syncthreads();
     int32_t* mine = hist + warp * E;
-    if (warp < warps) {
-        for (int64_t i = lo; i < hi; i += 32) {
-            const int32_t x = i + lane < hi ? e[i + lane] : -1;
-            const bool ok = x >= 0 && x < E;
-            const uint32_t same = __match_any_sync(0xffffffffu, ok ? x : -1);
-            if (ok && lane == __ffs(same) - 1) mine[x] += __popc(same);
+    for (int64_t i = lo; i < hi; i += 32 * MS_KEEP) {
+        if (!kept) fetch(i);
+#pragma unroll
+        for (int v = 0; v < MS_KEEP; v++) {
+            if (i + 32 * v >= hi) break;
+            const int32_t x = keep[v];
+            const uint32_t same = __match_any_sync(0xffffffffu, x);
+            if (x >= 0 && lane == __ffs(same) - 1) mine[x] += __popc(same);
             __syncwarp();
         }
     }
     __syncthreads();
     for (int x = tid; x < E; x += nthr) {
         int32_t s = 0;
+#pragma unroll 8
         for (int w = 0; w < warps; w++) {
             const int32_t h = hist[w * E + x];
             hist[w * E + x] = s;
@@ -69,16 +85,21 @@ __global__ void __launch_bounds__(1024)
         }
         tot[x] = s;
     }
-    cl.sync();
+    if (C > 1)
+        cl.sync();
+    else
+        __syncthreads();
     // experts in runs of `per` for every thread: the cluster's total of each, and its share below this block
     const int per = (E + nthr - 1) / nthr, x0 = min(E, tid * per), x1 = min(E, x0 + per);
     int32_t sum = 0;
     for (int x = x0; x < x1; x++) {
-        int32_t below = 0, all = 0;
-        for (int b = 0; b < C; b++) {
-            const int32_t v = cl.map_shared_rank(tot, b)[x];
-            all += v;
-            below += b < rank ? v : 0;
+        int32_t below = 0, all = 0, v[MS_MAX_CLUSTER];
+#pragma unroll
+        for (int b = 0; b < MS_MAX_CLUSTER; b++) v[b] = b < C ? cl.map_shared_rank(tot, b)[x] : 0;
+#pragma unroll
+        for (int b = 0; b < MS_MAX_CLUSTER; b++) {
+            all += v[b];
+            below += b < rank ? v[b] : 0;
         }
         first[x] = sum + below;
         sum += all;
@@ -99,18 +120,24 @@ __global__ void __launch_bounds__(1024)
         if (rank == 0) offsets[x + 1] += before;
     }
     if (rank == 0 && tid == 0) offsets[0] = 0;
-    cl.sync();  // every block has read the others' counts; `first` is complete
-    if (warp < warps) {
-        for (int64_t i = lo; i < hi; i += 32) {
-            const int32_t x = i + lane < hi ? e[i + lane] : -1;
-            const bool ok = x >= 0 && x < E;
-            const uint32_t same = __match_any_sync(0xffffffffu, ok ? x : -1);
+    // every block has read the others' counts; `first` is complete
+    if (C > 1)
+        cl.sync();
+    else
+        __syncthreads();
+    for (int64_t i = lo; i < hi; i += 32 * MS_KEEP) {
+        if (!kept) fetch(i);
+#pragma unroll
+        for (int v = 0; v < MS_KEEP; v++) {
+            if (i + 32 * v >= hi) break;
+            const int32_t x = keep[v];
+            const uint32_t same = __match_any_sync(0xffffffffu, x);
             int32_t p = -1;
-            if (ok) p = first[x] + mine[x] + __popc(same & ((1u << lane) - 1));
+            if (x >= 0) p = first[x] + mine[x] + __popc(same & ((1u << lane) - 1));
             __syncwarp();
-            if (ok && lane == __ffs(same) - 1) mine[x] += __popc(same);
+            if (x >= 0 && lane == __ffs(same) - 1) mine[x] += __popc(same);
             __syncwarp();
-            if (i + lane < hi) pos[i + lane] = p;
+            if (i + 32 * v + lane < hi) pos[i + 32 * v + lane] = p;
         }
     }
 }
@@ -119,52 +146,47 @@ __global__ void __launch_bounds__(1024)
 
 constexpr int MO_CHOICES = 4;  // positions (and weights) of a token kept in registers at a time
 
-// rows[pos[t][j]] = x[t] in units of VT; one token per tpr threads, blockIdx.y a share of the columns. U
+// rows[pos[t][j]] = x[t] in units of A bytes; one token per tpr threads, blockIdx.y a share of the columns. U
 // loads of a thread are in flight before its stores.
-template <typename VT, int U>
-__global__ void __launch_bounds__(256)
-    moe_dispatch_kernel(const char* __restrict__ x, int64_t T, int64_t nvec, int64_t ldx, const int32_t* __restrict__ pos,
+template <int A, int U>
+__global__ void __launch_bounds__(FP_ROW_THREADS)
+    moe_dispatch_kernel(const char* __restrict__ x, int64_t T, int nvec, int64_t ldx, const int32_t* __restrict__ pos,
                         int k, int64_t R, char* __restrict__ rows, int64_t ldr, int tpr) {
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
-    const VT* src = reinterpret_cast<const VT*>(x + t * ldx);
-    const int64_t step = (int64_t)tpr * gridDim.y, c0 = threadIdx.x % tpr + (int64_t)tpr * blockIdx.y;
-    for (int j0 = 0; j0 < k; j0 += MO_CHOICES) {
-        VT* dst[MO_CHOICES];
+    const char* src = x + t * ldx;
+    const int step = tpr * gridDim.y;
+    for (int c = threadIdx.x % tpr + tpr * blockIdx.y; c < nvec; c += U * step) {
+        FpWords<A> v[U];
 #pragma unroll
-        for (int j = 0; j < MO_CHOICES; j++) {
-            const int64_t p = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
-            dst[j] = p >= 0 && p < R ? reinterpret_cast<VT*>(rows + p * ldr) : nullptr;
-        }
-        for (int64_t c = c0; c < nvec; c += U * step) {
-            VT v[U];
+        for (int u = 0; u < U; u++)
+            if (c + u * step < nvec) v[u].load(src + (int64_t)(c + u * step) * A);
+        for (int j0 = 0; j0 < k; j0 += MO_CHOICES) {
+            char* dst[MO_CHOICES];
 #pragma unroll
-            for (int u = 0; u < U; u++)
-                if (c + u * step < nvec) v[u] = src[c + u * step];
+            for (int j = 0; j < MO_CHOICES; j++) {
+                const int64_t p = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
+                dst[j] = p >= 0 && p < R ? rows + p * ldr : nullptr;
+            }
 #pragma unroll
             for (int j = 0; j < MO_CHOICES; j++) {
                 if (!dst[j]) continue;
 #pragma unroll
                 for (int u = 0; u < U; u++)
-                    if (c + u * step < nvec) dst[j][c + u * step] = v[u];
+                    if (c + u * step < nvec) v[u].store(dst[j] + (int64_t)(c + u * step) * A);
             }
         }
     }
 }
 
-template <typename VT>
+template <int A>
 void launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, int64_t ldx, const int32_t* pos, int k,
                      int64_t R, void* rows, int64_t ldr, cudaStream_t st) {
-    constexpr int U = sizeof(VT) == 16 ? 4 : 8;
-    const int64_t nvec = bytes / (int64_t)sizeof(VT);
-    int tpr = 32;
-    while (tpr < 256 && tpr < nvec) tpr *= 2;
-    const int rpb = 256 / tpr;
-    const int64_t gx = (T + rpb - 1) / rpb;
-    // few tokens: their columns over more blocks
-    const int64_t gy = std::max<int64_t>(1, std::min((nvec + tpr - 1) / tpr, 4 * (int64_t)c->num_sms / gx));
-    moe_dispatch_kernel<VT, U><<<dim3((unsigned)gx, (unsigned)gy), 256, 0, st>>>((const char*)x, T, nvec, ldx, pos, k, R,
-                                                                             (char*)rows, ldr, tpr);
+    const int nvec = (int)(bytes / A);
+    constexpr int U = A == 16 ? 2 : 4;
+    const FpRowGrid g = fp_row_grid(c, T, nvec, U, true);
+    moe_dispatch_kernel<A, U><<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const char*)x, T, nvec, ldx, pos, k, R,
+                                                                        (char*)rows, ldr, g.tpr);
 }
 
 // ---- combine --------------------------------------------------------------------------------
@@ -172,136 +194,132 @@ void launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, i
 // out[t] = base[t] + sum_j w[t][j] rows[pos[t][j]] in fp32, rounded once; V elements per load, U vectors
 // of a thread at a time
 template <typename RT, typename OT, int V, int U>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(FP_ROW_THREADS)
     moe_combine_kernel(const RT* __restrict__ rows, int64_t R, int64_t ldr, const int32_t* __restrict__ pos,
-                       const float* __restrict__ w, const OT* base, int64_t ldb, int64_t T, int k, int64_t M, OT* out,
+                       const float* __restrict__ w, const OT* base, int64_t ldb, int64_t T, int k, int nvec, OT* out,
                        int64_t ldo, int tpr) {
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
-    const int64_t nvec = M / V, step = (int64_t)tpr * gridDim.y;
-    const FpVec<RT, V>* src[MO_CHOICES];
-    float s[MO_CHOICES];
-    auto choices = [&](int j0) {
-#pragma unroll
-        for (int j = 0; j < MO_CHOICES; j++) {
-            const int64_t p = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
-            src[j] = p >= 0 && p < R ? reinterpret_cast<const FpVec<RT, V>*>(rows + p * ldr) : nullptr;
-            s[j] = w && j0 + j < k ? __ldg(w + t * k + j0 + j) : 1.0f;
-        }
-    };
-    choices(0);
-    for (int64_t c = threadIdx.x % tpr + (int64_t)tpr * blockIdx.y; c < nvec; c += U * step) {
+    const int step = tpr * gridDim.y;
+    for (int c = threadIdx.x % tpr + tpr * blockIdx.y; c < nvec; c += U * step) {
         float acc[U][V];
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            FpVec<OT, V> b;
             const bool in = base && c + u * step < nvec;
-            if (in) b = *reinterpret_cast<const FpVec<OT, V>*>(base + t * ldb + (c + u * step) * V);
+            FpVec<OT, V> b;
+            if (in) b.load(base + t * ldb + (int64_t)(c + u * step) * V);
 #pragma unroll
-            for (int i = 0; i < V; i++) acc[u][i] = in ? fp_to_f(b.v[i]) : 0.0f;
+            for (int i = 0; i < V; i++) acc[u][i] = in ? b.get(i) : 0.0f;
         }
-        for (int j0 = 0; j0 < k; j0 += MO_CHOICES) {
-            if (k > MO_CHOICES) choices(j0);
-            // the loads of two choices at a time, then their sums in the order of the choices
+        // the loads of two choices at a time, then their sums in the order of the choices
+        for (int j0 = 0; j0 < k; j0 += 2) {
+            const RT* src[2];
+            float s[2];
+            FpVec<RT, V> v[2][U];
 #pragma unroll
-            for (int jj = 0; jj < MO_CHOICES; jj += 2) {
-                if (j0 + jj >= k) break;
-                FpVec<RT, V> v[2][U];
+            for (int j = 0; j < 2; j++) {
+                const int64_t p = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
+                src[j] = p >= 0 && p < R ? rows + p * ldr : nullptr;
+                s[j] = w && j0 + j < k ? __ldg(w + t * k + j0 + j) : 1.0f;
+            }
 #pragma unroll
-                for (int j = 0; j < 2; j++)
+            for (int j = 0; j < 2; j++)
 #pragma unroll
-                    for (int u = 0; u < U; u++)
-                        if (src[jj + j] && c + u * step < nvec) v[j][u] = src[jj + j][c + u * step];
+                for (int u = 0; u < U; u++)
+                    if (src[j] && c + u * step < nvec) v[j][u].load(src[j] + (int64_t)(c + u * step) * V);
 #pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    if (!src[jj + j]) continue;
+            for (int j = 0; j < 2; j++) {
+                if (!src[j]) continue;
 #pragma unroll
-                    for (int u = 0; u < U; u++)
+                for (int u = 0; u < U; u++)
 #pragma unroll
-                        for (int i = 0; i < V; i++) acc[u][i] = fmaf(s[jj + j], fp_to_f(v[j][u].v[i]), acc[u][i]);
-                }
+                    for (int i = 0; i < V; i++) acc[u][i] = fmaf(s[j], v[j][u].get(i), acc[u][i]);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; u++) {
             if (c + u * step >= nvec) break;
             FpVec<OT, V> o;
-#pragma unroll
-            for (int i = 0; i < V; i++) o.v[i] = fp_from_f<OT>(acc[u][i]);
-            *reinterpret_cast<FpVec<OT, V>*>(out + t * ldo + (c + u * step) * V) = o;
+            o.set(acc[u]);
+            o.store(out + t * ldo + (int64_t)(c + u * step) * V);
         }
     }
 }
 
 // ---- gradients of combine -------------------------------------------------------------------
 
-// One token per block: its k rows' gradients and the k inner products (fp32, a fixed order: a thread's
-// columns, then the block's tree). Two choices at a time read dout once.
+// One token per tpr threads: its k rows' gradients and the k inner products (fp32, a fixed order: a
+// thread's columns, its warp's tree, then the warps). Two choices at a time read dout once.
 template <typename RT, typename OT, int V, int U>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(FP_ROW_THREADS)
     moe_grad_kernel(const OT* __restrict__ dout, int64_t ldd, const RT* __restrict__ rows, int64_t R, int64_t ldr,
-                    const int32_t* __restrict__ pos, const float* __restrict__ w, int64_t T, int k, int64_t M,
-                    RT* __restrict__ drows, int64_t lddr, float* __restrict__ dw) {
-    __shared__ float red[2][8];
-    const int64_t t = blockIdx.x, nvec = M / V, step = blockDim.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const FpVec<OT, V>* g = reinterpret_cast<const FpVec<OT, V>*>(dout + t * ldd);
+                    const int32_t* __restrict__ pos, const float* __restrict__ w, int64_t T, int k, int nvec,
+                    RT* __restrict__ drows, int64_t lddr, float* __restrict__ dw, int tpr) {
+    __shared__ float red[2][32];
+    const int sub = threadIdx.x / tpr, tt = threadIdx.x % tpr, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + sub;
+    const bool live = t < T;
+    const OT* g = dout + (live ? t : 0) * ldd;
     for (int j0 = 0; j0 < k; j0 += 2) {
         int64_t p[2];
         float s[2], dot[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-            p[j] = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
+            p[j] = live && j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
             if (p[j] >= R) p[j] = -1;
-            s[j] = w && j0 + j < k ? __ldg(w + t * k + j0 + j) : 1.0f;
+            s[j] = w && live && j0 + j < k ? __ldg(w + t * k + j0 + j) : 1.0f;
         }
-        for (int64_t c = threadIdx.x; c < nvec && (p[0] >= 0 || p[1] >= 0); c += U * step) {
+        for (int c = tt; c < nvec && (p[0] >= 0 || p[1] >= 0); c += U * tpr) {
             FpVec<OT, V> gv[U];
             FpVec<RT, V> v[2][U];
 #pragma unroll
             for (int u = 0; u < U; u++)
-                if (c + u * step < nvec) gv[u] = g[c + u * step];
+                if (c + u * tpr < nvec) gv[u].load(g + (int64_t)(c + u * tpr) * V);
             if (dw) {
 #pragma unroll
                 for (int j = 0; j < 2; j++)
 #pragma unroll
                     for (int u = 0; u < U; u++)
-                        if (p[j] >= 0 && c + u * step < nvec)
-                            v[j][u] = reinterpret_cast<const FpVec<RT, V>*>(rows + p[j] * ldr)[c + u * step];
+                        if (p[j] >= 0 && c + u * tpr < nvec) v[j][u].load(rows + p[j] * ldr + (int64_t)(c + u * tpr) * V);
             }
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 if (p[j] < 0) continue;
 #pragma unroll
                 for (int u = 0; u < U; u++) {
-                    if (c + u * step >= nvec) break;
+                    if (c + u * tpr >= nvec) break;
                     if (dw) {
 #pragma unroll
-                        for (int i = 0; i < V; i++) dot[j] = fmaf(fp_to_f(gv[u].v[i]), fp_to_f(v[j][u].v[i]), dot[j]);
+                        for (int i = 0; i < V; i++) dot[j] = fmaf(gv[u].get(i), v[j][u].get(i), dot[j]);
                     }
                     if (drows) {
-                        FpVec<RT, V> o;
+                        float f[V];
 #pragma unroll
-                        for (int i = 0; i < V; i++) o.v[i] = fp_from_f<RT>(s[j] * fp_to_f(gv[u].v[i]));
-                        reinterpret_cast<FpVec<RT, V>*>(drows + p[j] * lddr)[c + u * step] = o;
+                        for (int i = 0; i < V; i++) f[i] = s[j] * gv[u].get(i);
+                        FpVec<RT, V> o;
+                        o.set(f);
+                        o.store(drows + p[j] * lddr + (int64_t)(c + u * tpr) * V);
                     }
                 }
             }
         }
         if (dw) {
-            if (j0) __syncthreads();  // red may still be read for the choices before
 #pragma unroll
-            for (int j = 0; j < 2; j++) {
+            for (int j = 0; j < 2; j++)
 #pragma unroll
                 for (int m = 16; m > 0; m >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], m);
-                if (lane == 0) red[j][warp] = dot[j];
+            float sum = lane ? dot[1] : dot[0];
+            if (tpr > 32) {
+                if (j0) __syncthreads();  // red may still be read for the choices before
+                if (lane < 2) red[lane][warp] = sum;
+                __syncthreads();
+                if (tt < 2) {
+                    sum = 0.0f;
+                    for (int i = 0; i < tpr >> 5; i++) sum += red[tt][sub * (tpr >> 5) + i];
+                }
             }
-            __syncthreads();
-            if (threadIdx.x < 2 && j0 + (int)threadIdx.x < k) {
-                float a = 0.0f;
-                for (int i = 0; i < (int)(blockDim.x >> 5); i++) a += red[threadIdx.x][i];
-                dw[t * k + j0 + threadIdx.x] = a;  // 0 where there is no row: nothing was added
-            }
+            // 0 where there is no row: nothing was added
+            if (live && tt < 2 && j0 + tt < k) dw[t * k + j0 + tt] = sum;
         }
     }
 }
@@ -386,15 +404,15 @@ int fp_moe_dispatch(fp_ctx* c, const void* x, int64_t T, int64_t row_bytes, int6
     int slot;
     fp_op_tic(c, st, K_MOE_DISPATCH, (double)row_bytes * (T + T * (double)k) + 4.0 * T * k, &slot);
     if (al >= 16)
-        launch_dispatch<uint4>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<16>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 8)
-        launch_dispatch<uint2>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<8>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 4)
-        launch_dispatch<uint32_t>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<4>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 2)
-        launch_dispatch<uint16_t>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<2>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else
-        launch_dispatch<uint8_t>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<1>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     fp_toc(c, st, slot);
     FP_CUDA(c, cudaGetLastError());
     return FP_OK;
@@ -432,18 +450,16 @@ int fp_moe_combine(fp_ctx* c, const void* rows, int rows_type, int64_t R, int64_
             const bool vec = M % V == 0 && fp_common_align({(uint64_t)(uintptr_t)rows, (uint64_t)ldr * rs}) == 16 &&
                              fp_common_align({(uint64_t)(uintptr_t)out, (uint64_t)(uintptr_t)base, (uint64_t)ldo * os,
                                               (uint64_t)ldb * os}) >= OA;
-            const int64_t nvec = vec ? M / V : M;
-            int tpr = 32;
-            while (tpr < 256 && tpr < nvec) tpr *= 2;
-            const int64_t gx = (T + 256 / tpr - 1) / (256 / tpr);
-            const int64_t gy = std::max<int64_t>(1, std::min((nvec + tpr - 1) / tpr, 4 * (int64_t)c->num_sms / gx));
-            const dim3 grid((unsigned)gx, (unsigned)gy);
-            if (vec)
-                moe_combine_kernel<RT, OT, V, 2><<<grid, 256, 0, st>>>((const RT*)rows, R, ldr, pos, weights,
-                                                                    (const OT*)base, ldb, T, k, M, (OT*)out, ldo, tpr);
+            const int nvec = (int)(vec ? M / V : M);
+            auto run = [&](auto kern, int loads) {
+                const FpRowGrid g = fp_row_grid(c, T, nvec, loads, true);
+                kern<<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const RT*)rows, R, ldr, pos, weights, (const OT*)base, ldb, T,
+                                                               k, nvec, (OT*)out, ldo, g.tpr);
+            };
+            if (vec)  // two loads in flight either way: of two choices, or of two vectors
+                k > 1 ? run(moe_combine_kernel<RT, OT, V, 1>, 1) : run(moe_combine_kernel<RT, OT, V, 2>, 2);
             else
-                moe_combine_kernel<RT, OT, 1, 8><<<grid, 256, 0, st>>>((const RT*)rows, R, ldr, pos, weights,
-                                                                    (const OT*)base, ldb, T, k, M, (OT*)out, ldo, tpr);
+                run(moe_combine_kernel<RT, OT, 1, 4>, 4);
         });
     });
     fp_toc(c, st, slot);
@@ -488,12 +504,13 @@ int fp_moe_combine_grad(fp_ctx* c, const void* dout, int out_type, int64_t ldd, 
                              fp_common_align({(uint64_t)(uintptr_t)rd, (uint64_t)(uintptr_t)drows, (uint64_t)ldr * rs,
                                               (uint64_t)lddr * rs}) == 16 &&
                              fp_common_align({(uint64_t)(uintptr_t)dout, (uint64_t)ldd * os}) >= OA;
-            if (vec)
-                moe_grad_kernel<RT, OT, V, 2><<<(unsigned)T, 256, 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos,
-                                                                        weights, T, k, M, (RT*)drows, lddr, dweights);
-            else
-                moe_grad_kernel<RT, OT, 1, 8><<<(unsigned)T, 256, 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos,
-                                                                        weights, T, k, M, (RT*)drows, lddr, dweights);
+            const int nvec = (int)(vec ? M / V : M);
+            auto run = [&](auto kern, int loads) {
+                const FpRowGrid g = fp_row_grid(c, T, nvec, loads, false);
+                kern<<<g.gx, g.threads(), 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k, nvec,
+                                                   (RT*)drows, lddr, dweights, g.tpr);
+            };
+            vec ? run(moe_grad_kernel<RT, OT, V, 1>, 1) : run(moe_grad_kernel<RT, OT, 1, 4>, 4);
         });
     });
     fp_toc(c, st, slot);

@@ -2,8 +2,9 @@
 //
 // a_t = max_j |x_tj|, scale_t = a_t / 127 (fp32), q_tj = the integer nearest to 127 x_tj / a_t, ties to
 // the even one. The integer is exact: a product with the fp32 value of 127 / a_t is off by less than
-// 127 * 2^-22, so only a value within 2^-14 of a half can round to the wrong side, and those compare
-// 254 |x| with (2 n + 1) a_t, whose products are exact in double.
+// 127 * 2^-22, so only a value within 2^-15 of a half can round to the wrong side, and those compare
+// 254 |x| with (2 n + 1) a_t, whose products are exact in double. Vectors with such a value (one value in
+// 16000) are noted by a bit and done again one value at a time after the others.
 //
 // A row with a NaN or an infinity has no scale: its scale is NaN and its integers are 0, so every
 // product with it is NaN. A row of zeros has scale 0.
@@ -13,71 +14,81 @@
 
 namespace {
 
-constexpr int QR_VALUES = 32;  // values of a row that a thread keeps in registers
 
+constexpr int QR_LOADS = 8;  // vectors of a row that a thread keeps in registers (single values: twice as many)
 constexpr float QR_MAGIC = 12582912.0f;  // 1.5 * 2^23: t + it has the nearest integer to t in its low bits
+constexpr float QR_NEAR = 0.5f - 3.0517578e-5f;
 
-// the integer nearest to 127 x / a for a value that lies next to a half (t: the approximate quotient)
-__device__ __noinline__ uint32_t quant_near_half(float x, float a, float t) {
-    const int n = (int)floorf(fabsf(t));
-    const double d = 254.0 * (double)fabsf(x) - (double)(2 * n + 1) * (double)a;
-    const int r = d > 0 ? n + 1 : d < 0 ? n : n + (n & 1);
-    return (uint32_t)(x < 0 ? -r : r);
-}
-
-// V values to int8
+// V values to int8 by the fp32 quotient (0 in a bad row); `near` is set when one lies next to a half
 template <typename T, int V>
-__device__ __forceinline__ FpVec<int8_t, V> quant_vec(const FpVec<T, V>& w, float up, float a, float inv) {
-    FpVec<int8_t, V> o;
-    bool near = false;
+__device__ __forceinline__ FpWords<V> quant_vec(const FpVec<T, V>& w, float inv, bool bad, bool& near) {
+    uint32_t r[V];
+    float off = 0.0f;
 #pragma unroll
     for (int e = 0; e < V; e++) {
-        const float t = fp_to_f(w.v[e]) * up * inv, r = t + QR_MAGIC;
-        o.v[e] = (int8_t)__float_as_uint(r);
-        near |= fabsf(t - (r - QR_MAGIC)) > 0.5f - 6.1035156e-5f;
+        const float t = w.get(e) * inv, n = t + QR_MAGIC;
+        r[e] = __float_as_uint(n);
+        off = fmaxf(off, fabsf(t - (n - QR_MAGIC)));
     }
-    if (near) {
+    near = off > QR_NEAR;
+    FpWords<V> o;
+    if constexpr (V == 1) {
+        o.w[0] = bad ? 0 : r[0];
+    } else {
 #pragma unroll
-        for (int e = 0; e < V; e++) {
-            const float x = fp_to_f(w.v[e]) * up, t = x * inv;
-            if (fabsf(t - (t + QR_MAGIC - QR_MAGIC)) > 0.5f - 6.1035156e-5f) o.v[e] = (int8_t)quant_near_half(x, a, t);
-        }
+        for (int i = 0; i < V / 4; i++)
+            o.w[i] = bad ? 0
+                         : __byte_perm(__byte_perm(r[4 * i], r[4 * i + 1], 0x0040),
+                                       __byte_perm(r[4 * i + 2], r[4 * i + 3], 0x0040), 0x5410);
     }
     return o;
 }
 
+// one value exactly
+__device__ __forceinline__ int8_t quant_exact(float x, float a) {
+    const float t = fabsf(x) * (127.0f / a);
+    int r = __float2int_rn(t);
+    if (fabsf(t - (float)r) > QR_NEAR) {
+        const int n = (int)floorf(t);
+        const double d = 254.0 * (double)fabsf(x) - (double)(2 * n + 1) * (double)a;
+        r = d > 0 ? n + 1 : d < 0 ? n : n + (n & 1);
+    }
+    return (int8_t)(x < 0 ? -r : r);
+}
+
 // One row per `tpr` threads (a multiple of 32 that divides the block). V: elements per load; a thread
-// keeps the first QR_VALUES / V vectors it reads, and reads what is beyond them a second time.
-template <typename T, int V>
-__global__ void __launch_bounds__(1024)
-    quant_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t K, int64_t ldx, const int32_t* __restrict__ pos,
-                      int k, int64_t R, int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale, int tpr,
-                      bool qvec) {
-    constexpr int NV = QR_VALUES / V;
+// keeps the first NV vectors it reads in registers, and reads what is beyond them a second time.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(512)
+    quant_rows_kernel(const T* __restrict__ x, int64_t rows, int K, int64_t ldx, const int32_t* __restrict__ pos, int k,
+                      int64_t R, int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale, int tpr, bool qvec) {
     __shared__ uint32_t red[32];
     const int sub = threadIdx.x / tpr, t = threadIdx.x % tpr, lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + sub;
     const bool live = row < rows;
     const T* xr = x + (live ? row : 0) * ldx;
-    const int64_t nvec = live ? K / V : 0;
+    const int nvec = live ? K / V : 0;
+    const int64_t p0 = !live ? -1 : pos ? __ldg(pos + row * k) : row;
     FpVec<T, V> reg[NV];
     uint32_t m = 0;  // the largest |x| as bits: NaN above infinity above every number
+    auto largest = [&](const FpVec<T, V>& w) {
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const int64_t c = t + (int64_t)i * tpr;
-        if (c < nvec) reg[i] = *reinterpret_cast<const FpVec<T, V>*>(xr + c * V);
-    }
+        for (int e = 0; e < V; e++) m = max(m, __float_as_uint(w.get(e)) & 0x7fffffffu);
+    };
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        if (t + (int64_t)i * tpr < nvec) {
+    for (int i = 0; i < NV; i++)
+        if (t + i * tpr < nvec) {
+            reg[i].load(xr + (t + i * tpr) * V);
+        } else {
 #pragma unroll
-            for (int e = 0; e < V; e++) m = max(m, __float_as_uint(fp_to_f(reg[i].v[e])) & 0x7fffffffu);
+            for (int e = 0; e < FpVec<T, V>::W; e++) reg[i].w[e] = 0;
         }
-    }
-    for (int64_t c = t + (int64_t)NV * tpr; c < nvec; c += tpr) {
-        const FpVec<T, V> w = *reinterpret_cast<const FpVec<T, V>*>(xr + c * V);
 #pragma unroll
-        for (int e = 0; e < V; e++) m = max(m, __float_as_uint(fp_to_f(w.v[e])) & 0x7fffffffu);
+    for (int i = 0; i < NV; i++) largest(reg[i]);
+    for (int c = t + NV * tpr; c < nvec; c += tpr) {
+        FpVec<T, V> w;
+        w.load(xr + c * V);
+        largest(w);
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (tpr > 32) {
@@ -89,40 +100,50 @@ __global__ void __launch_bounds__(1024)
     if (!live) return;
     const float amax = __uint_as_float(m);
     const bool bad = m >= 0x7f800000u;
-    // rows below 2^-64 are scaled up (exactly) so that 127 / a stays finite
-    const float up = amax < 5.421010862427522e-20f ? 18446744073709551616.0f : 1.0f;
-    const float a = amax * up;
-    const float inv = (bad || m == 0) ? 0.0f : 127.0f / a;
+    const float inv = bad || m == 0 ? 0.0f : 127.0f / amax;
+    // in rows below 2^-64 every value is done exactly, scaled up (127 / a may not be finite)
+    const bool tiny = amax < 5.421010862427522e-20f && m != 0;
+    const float up = tiny ? 18446744073709551616.0f : 1.0f;
     const int copies = pos ? k : 1;
-    if (t == 0) {
-        const float s = bad ? __uint_as_float(0x7fc00000u) : amax / 127.0f;
-        for (int j = 0; j < copies; j++) {
-            const int64_t p = pos ? pos[row * k + j] : row;
-            if (p >= 0 && p < R) scale[p] = s;
-        }
-    }
-    auto put = [&](int64_t c, const FpVec<T, V>& w) {
-        FpVec<int8_t, V> o = {};
-        if (inv != 0.0f) o = quant_vec<T, V>(w, up, a, inv);
-        for (int j = 0; j < copies; j++) {
-            const int64_t p = pos ? pos[row * k + j] : row;
-            if (p < 0 || p >= R) continue;
-            int8_t* d = q + p * ldq + c * V;
-            if (qvec) {
-                *reinterpret_cast<FpVec<int8_t, V>*>(d) = o;
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; e++) d[e] = o.v[e];
-            }
-        }
-    };
+    FpWords<V> o[NV];
+    uint32_t redo = 0;  // the vectors with a value next to a half
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-        const int64_t c = t + (int64_t)i * tpr;
-        if (c < nvec) put(c, reg[i]);
+        bool near;
+        o[i] = quant_vec<T, V>(reg[i], tiny ? 0.0f : inv, bad, near);
+        if (near || tiny) redo |= 1u << i;
     }
-    for (int64_t c = t + (int64_t)NV * tpr; c < nvec; c += tpr)
-        put(c, *reinterpret_cast<const FpVec<T, V>*>(xr + c * V));
+    for (int j = 0; j < copies; j++) {
+        const int64_t p = j == 0 ? p0 : __ldg(pos + row * k + j);
+        if (p < 0 || p >= R) continue;
+        if (t == 0) scale[p] = bad ? __uint_as_float(0x7fc00000u) : amax / 127.0f;
+        int8_t* d = q + p * ldq;
+        auto put = [&](int c, const FpWords<V>& w) {
+            if (V == 1 || qvec) {
+                w.store(d + c * V);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; e++) d[c * V + e] = (int8_t)(w.w[e >> 2] >> (8 * (e & 3)));
+            }
+        };
+        auto again = [&](int c) {
+            for (int e = 0; e < V; e++) d[c * V + e] = quant_exact(fp_to_f(xr[c * V + e]) * up, amax * up);
+        };
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (t + i * tpr < nvec) put(t + i * tpr, o[i]);
+        for (uint32_t left = redo; left; left &= left - 1) {
+            const int c = t + (__ffs(left) - 1) * tpr;
+            if (c < nvec) again(c);
+        }
+        for (int c = t + NV * tpr; c < nvec; c += tpr) {
+            FpVec<T, V> w;
+            w.load(xr + c * V);
+            bool near;
+            put(c, quant_vec<T, V>(w, tiny ? 0.0f : inv, bad, near));
+            if (near || tiny) again(c);
+        }
+    }
 }
 
 template <typename T>
@@ -132,17 +153,15 @@ void launch_quant(const fp_ctx* c, const void* x, int64_t T_, int64_t K, int64_t
     const bool vec = fp_common_align({(uint64_t)(uintptr_t)x, (uint64_t)ldx * sizeof(T), (uint64_t)K * sizeof(T)}) == 16;
     const bool qvec = fp_common_align({(uint64_t)(uintptr_t)q, (uint64_t)ldq}) >= V;
     const int64_t nvec = vec ? K / V : K;
-    const int nv = QR_VALUES / (vec ? V : 1);
-    // enough threads to hold the row in registers; more while the rows alone do not fill the GPU
-    int tpr = 32;
-    while (tpr < 1024 && (int64_t)tpr * nv < nvec) tpr *= 2;
-    while (tpr < 1024 && tpr < nvec && T_ * tpr < (int64_t)c->num_sms * 512) tpr *= 2;
-    const int threads = std::max(tpr, 128), rpb = threads / tpr;
-    const unsigned grid = (unsigned)((T_ + rpb - 1) / rpb);
-    if (vec)
-        quant_rows_kernel<T, V><<<grid, threads, 0, st>>>((const T*)x, T_, K, ldx, pos, k, R, q, ldq, scale, tpr, qvec);
-    else
-        quant_rows_kernel<T, 1><<<grid, threads, 0, st>>>((const T*)x, T_, K, ldx, pos, k, R, q, ldq, scale, tpr, true);
+    // a few warps hold a row in registers, so that many rows are in flight; few rows: a vector a thread
+    auto run = [&](auto kern, int loads) {
+        int tpr = 32;
+        while (tpr < 512 && ((int64_t)tpr * loads < nvec || (T_ * tpr < (int64_t)c->num_sms * 256 && tpr < nvec))) tpr += 32;
+        const int threads = std::max(128 / tpr, 1) * tpr;
+        const unsigned grid = (unsigned)((T_ + threads / tpr - 1) / (threads / tpr));
+        kern<<<grid, threads, 0, st>>>((const T*)x, T_, (int)K, ldx, pos, k, R, q, ldq, scale, tpr, qvec || !vec);
+    };
+    vec ? run(quant_rows_kernel<T, V, QR_LOADS>, QR_LOADS) : run(quant_rows_kernel<T, 1, 2 * QR_LOADS>, 2 * QR_LOADS);
 }
 
 }  // namespace
