@@ -24,15 +24,15 @@ namespace {
 // ---- sort -----------------------------------------------------------------------------------
 //
 // One thread-block cluster ranks all choices. Warp w of the cluster takes a run of consecutive
-// choices and counts them by expert in a histogram of its own in shared memory; the histograms'
-// prefix sums (over a block's warps, then over the cluster's blocks through distributed shared
-// memory, then over the experts) give every warp the first row of each expert that is its own, and a
-// second pass over its run hands them out. The lanes of a warp that hold the same expert are found by
-// match.any; the order within a warp is the lanes', so the sort is stable.
+// choices and ranks them by expert against a histogram of its own in shared memory: the lanes that hold the
+// same expert are found by match.any and take the ranks after the histogram's count in the order of the
+// lanes, so the sort is stable. The histograms' prefix sums (over a block's warps, then over the cluster's
+// blocks through distributed shared memory, then over the experts) give every warp its first row of each
+// expert, which a second pass over the run adds to the ranks.
 constexpr int MS_HIST_BYTES = 176 * 1024;
 constexpr int MS_MAX_CLUSTER = 8;
 
-constexpr int MS_KEEP = 8;  // choices of a lane that stay in registers between the passes
+constexpr int MS_KEEP = 8;  // choices of a lane that stay in registers between the passes (of longer runs, ranks in pos)
 
 __global__ void __launch_bounds__(1024)
     moe_sort_kernel(const int32_t* __restrict__ e, int64_t n, int E, int warps, int32_t* __restrict__ offsets,
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(1024)
     const int64_t run = ((n + (int64_t)C * warps - 1) / ((int64_t)C * warps) + 31) / 32 * 32;
     const int64_t lo = warp < warps ? min(n, ((int64_t)rank * warps + warp) * run) : n, hi = min(n, lo + run);
     const bool kept = run <= 32 * MS_KEEP;
-    int32_t keep[MS_KEEP];  // -1: none
+    int32_t keep[MS_KEEP], rank_in[MS_KEEP];  // the experts (-1: none) and the ranks among the run's of an expert
     auto fetch = [&](int64_t i) {
 #pragma unroll
         for (int v = 0; v < MS_KEEP; v++) {
@@ -68,10 +68,18 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
         for (int v = 0; v < MS_KEEP; v++) {
             if (i + 32 * v >= hi) break;
+            // the choice's rank among the run's of its expert
             const int32_t x = keep[v];
             const uint32_t same = __match_any_sync(0xffffffffu, x);
-            if (x >= 0 && lane == __ffs(same) - 1) mine[x] += __popc(same);
+            int32_t r = 0;
+            if (x >= 0) r = mine[x] + __popc(same & ((1u << lane) - 1));
             __syncwarp();
+            if (x >= 0 && lane == __ffs(same) - 1) mine[x] = r + __popc(same);
+            __syncwarp();
+            if (kept)
+                rank_in[v] = r;
+            else if (i + 32 * v + lane < hi)
+                pos[i + 32 * v + lane] = r;
         }
     }
     __syncthreads();
@@ -130,14 +138,9 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
         for (int v = 0; v < MS_KEEP; v++) {
             if (i + 32 * v >= hi) break;
+            const int64_t at = i + 32 * v + lane;
             const int32_t x = keep[v];
-            const uint32_t same = __match_any_sync(0xffffffffu, x);
-            int32_t p = -1;
-            if (x >= 0) p = first[x] + mine[x] + __popc(same & ((1u << lane) - 1));
-            __syncwarp();
-            if (x >= 0 && lane == __ffs(same) - 1) mine[x] += __popc(same);
-            __syncwarp();
-            if (i + 32 * v + lane < hi) pos[i + 32 * v + lane] = p;
+            if (at < hi) pos[at] = x < 0 ? -1 : first[x] + mine[x] + (kept ? rank_in[v] : pos[at]);
         }
     }
 }

@@ -2,9 +2,8 @@
 //
 // a_t = max_j |x_tj|, scale_t = a_t / 127 (fp32), q_tj = the integer nearest to 127 x_tj / a_t, ties to
 // the even one. The integer is exact: a product with the fp32 value of 127 / a_t is off by less than
-// 127 * 2^-22, so only a value within 2^-15 of a half can round to the wrong side, and those compare
-// 254 |x| with (2 n + 1) a_t, whose products are exact in double. Vectors with such a value (one value in
-// 16000) are noted by a bit and done again one value at a time after the others.
+// 127 * 2^-23, so only a value within 2^-15 of a half can round to the wrong side, and those compare
+// 254 |x| with (2 n + 1) a_t, products that are exact in fp32 for 16-bit values and in double for others.
 //
 // A row with a NaN or an infinity has no scale: its scale is NaN and its integers are 0, so every
 // product with it is NaN. A row of zeros has scale 0.
@@ -15,51 +14,84 @@
 namespace {
 
 
-constexpr int QR_LOADS = 8;  // vectors of a row that a thread keeps in registers (single values: twice as many)
+constexpr int QR_LOADS = 8;              // vectors of a row that a thread keeps in registers (single values: twice as many)
 constexpr float QR_MAGIC = 12582912.0f;  // 1.5 * 2^23: t + it has the nearest integer to t in its low bits
 constexpr float QR_NEAR = 0.5f - 3.0517578e-5f;
 
-// V values to int8 by the fp32 quotient (0 in a bad row); `near` is set when one lies next to a half
+// what a row's values are divided by: 127 / a, and the row scaled by 2^64 where 127 / a may not be finite
+struct QuantRow {
+    float inv;         // of the fast quotient; 0 in a row of zeros, with a NaN or an infinity, or scaled up
+    float up, a, inv_up;  // 1 or 2^64; a up; 127 / (a up)
+    bool bad;          // integers 0
+    bool tiny;         // scaled up: every value exactly
+};
+
+// x's integer as a float: the nearest to t = 127 x / a unless t lies next to a half, then by 254 |x| - (2 n + 1) a
+template <typename T>
+__device__ __forceinline__ float quant_exact(float x, const QuantRow& row) {
+    const float ax = fabsf(x) * row.up, t = ax * row.inv_up, r = (t + QR_MAGIC) - QR_MAGIC;
+    float n = r;
+    if (fabsf(t - r) > QR_NEAR) {
+        n = t > r ? r : r - 1.0f;
+        bool above, tie;
+        if constexpr (sizeof(T) == 2) {  // at most 11 + 8 bits: both products are exact
+            const float d = 254.0f * ax - (2.0f * n + 1.0f) * row.a;
+            above = d > 0.0f, tie = d == 0.0f;
+        } else {
+            const double d = 254.0 * (double)ax - (double)(2.0f * n + 1.0f) * (double)row.a;
+            above = d > 0.0, tie = d == 0.0;
+        }
+        if (above || (tie && ((int)n & 1))) n += 1.0f;
+    }
+    return copysignf(n, x);
+}
+
+// V values to int8
 template <typename T, int V>
-__device__ __forceinline__ FpWords<V> quant_vec(const FpVec<T, V>& w, float inv, bool bad, bool& near) {
-    uint32_t r[V];
-    float off = 0.0f;
+__device__ __forceinline__ FpWords<V> quant_vec(const FpVec<T, V>& w, const QuantRow& row) {
+    float n[V], off = 0.0f;
 #pragma unroll
     for (int e = 0; e < V; e++) {
-        const float t = w.get(e) * inv, n = t + QR_MAGIC;
-        r[e] = __float_as_uint(n);
-        off = fmaxf(off, fabsf(t - (n - QR_MAGIC)));
+        const float t = w.get(e) * row.inv;
+        n[e] = t + QR_MAGIC;
+        off = fmaxf(off, fabsf(t - (n[e] - QR_MAGIC)));
     }
-    near = off > QR_NEAR;
+    if (off > QR_NEAR || row.tiny) {
+#pragma unroll
+        for (int e = 0; e < V; e++) n[e] = quant_exact<T>(w.get(e), row) + QR_MAGIC;
+    }
     FpWords<V> o;
     if constexpr (V == 1) {
-        o.w[0] = bad ? 0 : r[0];
+        o.w[0] = row.bad ? 0 : __float_as_uint(n[0]);
     } else {
 #pragma unroll
         for (int i = 0; i < V / 4; i++)
-            o.w[i] = bad ? 0
-                         : __byte_perm(__byte_perm(r[4 * i], r[4 * i + 1], 0x0040),
-                                       __byte_perm(r[4 * i + 2], r[4 * i + 3], 0x0040), 0x5410);
+            o.w[i] = row.bad ? 0
+                             : __byte_perm(__byte_perm(__float_as_uint(n[4 * i]), __float_as_uint(n[4 * i + 1]), 0x0040),
+                                           __byte_perm(__float_as_uint(n[4 * i + 2]), __float_as_uint(n[4 * i + 3]), 0x0040),
+                                           0x5410);
     }
     return o;
 }
 
-// one value exactly
-__device__ __forceinline__ int8_t quant_exact(float x, float a) {
-    const float t = fabsf(x) * (127.0f / a);
-    int r = __float2int_rn(t);
-    if (fabsf(t - (float)r) > QR_NEAR) {
-        const int n = (int)floorf(t);
-        const double d = 254.0 * (double)fabsf(x) - (double)(2 * n + 1) * (double)a;
-        r = d > 0 ? n + 1 : d < 0 ? n : n + (n & 1);
+// The largest magnitude of values as bits of T (NaN above infinity above every number), two 16-bit values
+// to a word
+template <typename T, int V>
+__device__ __forceinline__ uint32_t quant_largest(const FpVec<T, V>& w, uint32_t m) {
+#pragma unroll
+    for (int i = 0; i < FpVec<T, V>::W; i++) {
+        if constexpr (sizeof(T) == 4)
+            m = max(m, w.w[i] & 0x7fffffffu);
+        else
+            m = __vmaxu2(m, w.w[i] & 0x7fff7fffu);
     }
-    return (int8_t)(x < 0 ? -r : r);
+    return m;
 }
 
 // One row per `tpr` threads (a multiple of 32 that divides the block). V: elements per load; a thread
 // keeps the first NV vectors it reads in registers, and reads what is beyond them a second time.
 template <typename T, int V, int NV>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(256, 4)
     quant_rows_kernel(const T* __restrict__ x, int64_t rows, int K, int64_t ldx, const int32_t* __restrict__ pos, int k,
                       int64_t R, int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale, int tpr, bool qvec) {
     __shared__ uint32_t red[32];
@@ -70,26 +102,24 @@ __global__ void __launch_bounds__(512)
     const int nvec = live ? K / V : 0;
     const int64_t p0 = !live ? -1 : pos ? __ldg(pos + row * k) : row;
     FpVec<T, V> reg[NV];
-    uint32_t m = 0;  // the largest |x| as bits: NaN above infinity above every number
-    auto largest = [&](const FpVec<T, V>& w) {
 #pragma unroll
-        for (int e = 0; e < V; e++) m = max(m, __float_as_uint(w.get(e)) & 0x7fffffffu);
-    };
-#pragma unroll
-    for (int i = 0; i < NV; i++)
+    for (int i = 0; i < NV; i++) {
         if (t + i * tpr < nvec) {
             reg[i].load(xr + (t + i * tpr) * V);
         } else {
 #pragma unroll
             for (int e = 0; e < FpVec<T, V>::W; e++) reg[i].w[e] = 0;
         }
+    }
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < NV; i++) largest(reg[i]);
+    for (int i = 0; i < NV; i++) m = quant_largest<T, V>(reg[i], m);
     for (int c = t + NV * tpr; c < nvec; c += tpr) {
         FpVec<T, V> w;
         w.load(xr + c * V);
-        largest(w);
+        m = quant_largest<T, V>(w, m);
     }
+    if (sizeof(T) == 2) m = max(m >> 16, m & 0xffffu);
     m = __reduce_max_sync(0xffffffffu, m);
     if (tpr > 32) {
         if (lane == 0) red[threadIdx.x >> 5] = m;
@@ -98,25 +128,24 @@ __global__ void __launch_bounds__(512)
         m = __reduce_max_sync(0xffffffffu, red[w0 + (lane < nw ? lane : 0)]);
     }
     if (!live) return;
-    const float amax = __uint_as_float(m);
-    const bool bad = m >= 0x7f800000u;
-    const float inv = bad || m == 0 ? 0.0f : 127.0f / amax;
-    // in rows below 2^-64 every value is done exactly, scaled up (127 / a may not be finite)
-    const bool tiny = amax < 5.421010862427522e-20f && m != 0;
-    const float up = tiny ? 18446744073709551616.0f : 1.0f;
+    FpVec<T, 1> top;
+    top.w[0] = m;
+    const float amax = top.get(0);
+    QuantRow r;
+    r.bad = !(amax < __uint_as_float(0x7f800000u));  // an infinity or NaN
+    r.tiny = amax < 5.421010862427522e-20f && m != 0;  // 2^-64
+    r.up = r.tiny ? 18446744073709551616.0f : 1.0f;
+    r.a = amax * r.up;
+    r.inv_up = r.bad || m == 0 ? 0.0f : 127.0f / r.a;
+    r.inv = r.tiny ? 0.0f : r.inv_up;
     const int copies = pos ? k : 1;
     FpWords<V> o[NV];
-    uint32_t redo = 0;  // the vectors with a value next to a half
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        bool near;
-        o[i] = quant_vec<T, V>(reg[i], tiny ? 0.0f : inv, bad, near);
-        if (near || tiny) redo |= 1u << i;
-    }
+    for (int i = 0; i < NV; i++) o[i] = quant_vec<T, V>(reg[i], r);
     for (int j = 0; j < copies; j++) {
         const int64_t p = j == 0 ? p0 : __ldg(pos + row * k + j);
         if (p < 0 || p >= R) continue;
-        if (t == 0) scale[p] = bad ? __uint_as_float(0x7fc00000u) : amax / 127.0f;
+        if (t == 0) scale[p] = r.bad ? __uint_as_float(0x7fc00000u) : amax / 127.0f;
         int8_t* d = q + p * ldq;
         auto put = [&](int c, const FpWords<V>& w) {
             if (V == 1 || qvec) {
@@ -126,22 +155,13 @@ __global__ void __launch_bounds__(512)
                 for (int e = 0; e < V; e++) d[c * V + e] = (int8_t)(w.w[e >> 2] >> (8 * (e & 3)));
             }
         };
-        auto again = [&](int c) {
-            for (int e = 0; e < V; e++) d[c * V + e] = quant_exact(fp_to_f(xr[c * V + e]) * up, amax * up);
-        };
 #pragma unroll
         for (int i = 0; i < NV; i++)
             if (t + i * tpr < nvec) put(t + i * tpr, o[i]);
-        for (uint32_t left = redo; left; left &= left - 1) {
-            const int c = t + (__ffs(left) - 1) * tpr;
-            if (c < nvec) again(c);
-        }
         for (int c = t + NV * tpr; c < nvec; c += tpr) {
             FpVec<T, V> w;
             w.load(xr + c * V);
-            bool near;
-            put(c, quant_vec<T, V>(w, tiny ? 0.0f : inv, bad, near));
-            if (near || tiny) again(c);
+            put(c, quant_vec<T, V>(w, r));
         }
     }
 }
@@ -156,7 +176,7 @@ void launch_quant(const fp_ctx* c, const void* x, int64_t T_, int64_t K, int64_t
     // a few warps hold a row in registers, so that many rows are in flight; few rows: a vector a thread
     auto run = [&](auto kern, int loads) {
         int tpr = 32;
-        while (tpr < 512 && ((int64_t)tpr * loads < nvec || (T_ * tpr < (int64_t)c->num_sms * 256 && tpr < nvec))) tpr += 32;
+        while (tpr < 256 && ((int64_t)tpr * loads < nvec || (T_ * tpr < (int64_t)c->num_sms * 256 && tpr < nvec))) tpr += 32;
         const int threads = std::max(128 / tpr, 1) * tpr;
         const unsigned grid = (unsigned)((T_ + threads / tpr - 1) / (threads / tpr));
         kern<<<grid, threads, 0, st>>>((const T*)x, T_, (int)K, ldx, pos, k, R, q, ldq, scale, tpr, qvec || !vec);
