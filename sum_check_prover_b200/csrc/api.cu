@@ -75,6 +75,18 @@ fp_ctx* fp_ctx_create(int device) {
         return nullptr;
     }
     memset((void*)c->mb, 0, sizeof(FpMailbox));
+    // a pool that keeps what it was given; without one (NULL) only operands with odd pitches are refused
+    cudaMemPoolProps pp = {};
+    pp.allocType = cudaMemAllocationTypePinned;
+    pp.location.type = cudaMemLocationTypeDevice;
+    pp.location.id = device;
+    uint64_t keep = ~0ull;
+    if (cudaMemPoolCreate(&c->pool, &pp) != cudaSuccess ||
+        cudaMemPoolSetAttribute(c->pool, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess) {
+        cudaGetLastError();
+        if (c->pool) cudaMemPoolDestroy(c->pool);
+        c->pool = nullptr;
+    }
     // A profiler that replays kernels holds the host inside the launch call, so
     // a kernel that waits for the host's challenges could never be answered:
     // under an injected profiler (or FP_STEPPED=1) every round is its own launch.
@@ -106,6 +118,7 @@ void fp_ctx_destroy(fp_ctx* c) {
     if (c->tickets) cudaFree(c->tickets);
     if (c->relay) cudaFree(c->relay);
     if (c->mb) cudaFreeHost(c->mb);
+    if (c->pool) cudaMemPoolDestroy(c->pool);
     delete c;
 }
 
@@ -411,7 +424,7 @@ const char* fp_kernel_name(int k) {
         "route_witness", "route_vectors", "route_open", "route_round", "route_final",
         "lhi2_column", "lhi2_round", "lhi2_final", "silu2_tree", "silu2_round", "silu2_leaf",
         "lu2_hist", "lu2_tree", "lu2_round", "lu2_leaf", "lhr_column", "lhr_round", "lhr_final", "dsp_claim",
-        "dsp_vectors", "silu_inputs", "ffn_hidden", "scl_group", "quant_rows", "matmul_i8", "moe_sort", "moe_dispatch",
+        "dsp_vectors", "silu_inputs", "ffn_hidden", "scl_group", "quant_rows", "matmul_i8", "realign_rows", "moe_sort", "moe_dispatch",
         "moe_combine", "moe_grad"};
     return (k >= 0 && k < K_COUNT) ? names[k] : "?";
 }

@@ -76,6 +76,7 @@ enum FpKernel {
     K_SCL_GROUP,
     K_QUANT_ROWS,
     K_MATMUL_I8,
+    K_REALIGN,
     K_MOE_SORT,
     K_MOE_DISPATCH,
     K_MOE_COMBINE,
@@ -136,6 +137,7 @@ struct fp_ctx {
     // unscaled sites, 0 mma.sync (FP_TCGEN05 selects 0 or 1)
     int tc_gemm = 2;
     FpMmPoint mm_point;
+    cudaMemPool_t pool = nullptr;  // stream-ordered scratch of operators (rows that TMA cannot read)
     uint32_t op_smem = 0;  // operator kernels whose shared-memory limit has been raised on this device, a bit each
     // timing
     int profiling = 0;

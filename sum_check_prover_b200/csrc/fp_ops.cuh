@@ -96,6 +96,31 @@ __device__ __forceinline__ __half fp_from_f<__half>(float x) { return __float2ha
 template <>
 __device__ __forceinline__ __nv_bfloat16 fp_from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// the bytes of a matrix that may be read: from its first value to its last
+struct FpSpan {
+    const char *lo, *hi;
+};
+template <typename T>
+__device__ __forceinline__ FpSpan fp_span(const T* p, int64_t rows, int64_t ld, int64_t cols) {
+    return FpSpan{reinterpret_cast<const char*>(p), reinterpret_cast<const char*>(p + (rows - 1) * ld + cols)};
+}
+
+// 16 bytes from any address: the two aligned 16 bytes that they lie in, shifted. False where those are not
+// both inside the span (the matrix's ends).
+__device__ __forceinline__ bool fp_load16_any(const void* p, const FpSpan& span, uint32_t (&o)[4]) {
+    const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    const char* q = reinterpret_cast<const char*>(p) - sh;
+    if (q < span.lo || q + 32 > span.hi) return false;
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(q)), b = __ldg(reinterpret_cast<const uint4*>(q) + 1);
+    uint32_t w[7] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+    if (sh & 8) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = b.w;
+    if (sh & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
+    const uint32_t bits = 8 * (sh & 3);
+#pragma unroll
+    for (int i = 0; i < 4; i++) o[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    return true;
+}
+
 // BYTES consecutive bytes as words (a lone 1 or 2 bytes in one), loaded and stored in units of up to 16
 template <int BYTES>
 struct FpWords {
@@ -119,6 +144,36 @@ struct FpWords {
             w[0] = *reinterpret_cast<const uint8_t*>(p);
         }
     }
+    // from any address that is a multiple of UNIT
+    template <int UNIT>
+    __device__ __forceinline__ void load_any(const void* p, const FpSpan& span) {
+        if constexpr (BYTES % 16 == 0) {
+            bool ok = true;
+#pragma unroll
+            for (int i = 0; i < BYTES / 16; i++) {
+                uint32_t o[4] = {0, 0, 0, 0};
+                ok = ok && fp_load16_any(reinterpret_cast<const char*>(p) + 16 * i, span, o);
+#pragma unroll
+                for (int j = 0; j < 4; j++) w[4 * i + j] = o[j];
+            }
+            if (ok) return;
+        }
+        if constexpr (UNIT == 4) {
+#pragma unroll
+            for (int i = 0; i < W; i++) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        } else if constexpr (UNIT == 2) {
+#pragma unroll
+            for (int i = 0; i < W; i++)
+                w[i] = (uint32_t) reinterpret_cast<const uint16_t*>(p)[2 * i] | (uint32_t) reinterpret_cast<const uint16_t*>(p)[2 * i + 1] << 16;
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; i++) {
+                w[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; j++) w[i] |= (uint32_t) reinterpret_cast<const uint8_t*>(p)[4 * i + j] << (8 * j);
+            }
+        }
+    }
     __device__ __forceinline__ void store(void* p) const {
         if constexpr (BYTES >= 16) {
 #pragma unroll
@@ -139,6 +194,14 @@ struct FpWords {
 // V consecutive real values
 template <typename T, int V>
 struct FpVec : FpWords<V * (int)sizeof(T)> {
+    // ANY: from any multiple of the element's size
+    template <bool ANY>
+    __device__ __forceinline__ void load_row(const T* p, const FpSpan& span) {
+        if constexpr (ANY)
+            this->template load_any<(int)sizeof(T)>(p, span);
+        else
+            this->load(p);
+    }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(T) == 4) {
             return __uint_as_float(this->w[i]);

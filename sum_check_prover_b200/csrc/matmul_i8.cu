@@ -12,11 +12,10 @@
 //                      (XB rows each), 128-byte swizzle: the MMA's K-major layout.
 //   warp 1             four K = 32 MMAs per k-tile, committed to the stage; the tile's last k-tile to the
 //                      accumulator slot's barrier (two slots: the next tile's MMAs run during the epilogue).
-//   warps 2-5          epilogue: tcgen05.ld, both scales, conversion, stores (32 channels of one token a
+//   warps 2-9          epilogue: tcgen05.ld, both scales, conversion, stores (32 channels of one token a
 //                      warp and store).
-//   warps 6-21         (COPY) operands that TMA cannot read, because their address or pitch is not a multiple
-//                      of 16: four groups of four warps take every fourth k-tile each, read it with word loads,
-//                      realign it in registers and write the same swizzled layout.
+// PAIR: two blocks (cta_group::2) share a tile of 256 channels by 256 tokens: each loads its 128 channels and
+// half of the tokens, one issues the MMAs of both.
 // Blocks are persistent, one per SM, and walk the tiles of all experts (channels fastest, so that blocks
 // that run together share a group's tokens); the experts' tile counts come from the offsets on the device.
 //
@@ -39,24 +38,21 @@ constexpr int MI_BK = 128;                  // bytes of K per k-tile
 constexpr int MI_W_BYTES = MI_BM * MI_BK;   // the weight box
 constexpr int MI_MAX_STAGES = 12;
 constexpr int MI_SMEM = 220 * 1024;         // dynamic shared memory of a block that has its SM alone
-constexpr int MI_COPY_GROUPS = 4;
-constexpr int MI_BASE_THREADS = 192;
+constexpr int MI_EPI_WARPS = 8;
+constexpr int MI_THREADS = 32 * (2 + MI_EPI_WARPS);
 constexpr uint32_t MI_WAIT_LIMIT = 1u << 24;
 
 __host__ __device__ constexpr int mi_box_rows(int bn) { return bn >= 256 ? 64 : 32; }  // rows of a token box
 
 struct alignas(64) MiArgs {
     CUtensorMap tw, tx;  // E M rows of K bytes, boxes of 128 rows; N rows of K bytes, boxes of XB rows
-    const int8_t* w;
     const float* w_scale;
-    const int8_t* x;
     const float* x_scale;
     const int32_t* offsets;
     void* y;
-    int64_t ldw, ldx, ldy;
+    int64_t ldy;
     int32_t M, K, N, E;
     int32_t y_type;
-    int32_t copy_w, copy_x;  // (COPY) which operands TMA does not read
     int32_t mt;              // channel tiles of an expert
     int32_t nk;              // k-tiles
     int32_t stages;
@@ -192,56 +188,6 @@ __device__ __forceinline__ void mi_ld8(uint32_t a, int32_t (&v)[8]) {
 }
 __device__ __forceinline__ void mi_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 
-// 16 bytes at p, of which the first `valid` (<= 16) are wanted and the others 0: aligned words inside
-// [base, end), the bytes that the operand's rows span, or single bytes at its two ends
-__device__ __forceinline__ uint4 mi_load16(const int8_t* p, int valid, const int8_t* base, const int8_t* end) {
-    uint32_t o[4] = {0, 0, 0, 0};
-    if (valid > 0) {
-        const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3);
-        const int8_t* q = p - sh;
-        if (q >= base && q + 20 <= end) {
-            const uint32_t* qw = reinterpret_cast<const uint32_t*>(q);
-            uint32_t u[5];
-#pragma unroll
-            for (int i = 0; i < 5; i++) u[i] = __ldg(qw + i);
-#pragma unroll
-            for (int i = 0; i < 4; i++) o[i] = __funnelshift_r(u[i], u[i + 1], 8 * sh);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; i++)
-                if (i < valid) o[i >> 2] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
-        }
-        if (valid < 16) {
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int left = valid - 4 * i;
-                o[i] &= left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
-            }
-        }
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
-// one k-tile of `rows` rows (r0 the first, those past `lim` zero) into the swizzled layout, by 128 threads
-__device__ __forceinline__ void mi_copy_tile(const int8_t* base, int64_t ld, int64_t total_rows, int64_t r0, int rows,
-                                             int64_t lim, int k0, int K, uint8_t* dst, int t) {
-    const int8_t* end = base + (total_rows - 1) * ld + K;
-    const int kk = t & 7, valid = min(16, K - k0 - 16 * kk);
-#pragma unroll 1
-    for (int r = t >> 3; r < rows; r += 64) {
-        uint4 v[4];
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-            const int64_t row = r0 + r + 16 * u;
-            const bool ok = r + 16 * u < rows && row < lim;
-            v[u] = mi_load16(base + (ok ? row * ld + k0 + 16 * kk : 0), ok ? valid : 0, base, end);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; u++)
-            if (r + 16 * u < rows) *reinterpret_cast<uint4*>(dst + mi_off(r + 16 * u, kk)) = v[u];
-    }
-}
-
 // the tokens of token tile u: expert e's rows [first[e], first[e + 1]) in equal shares of a multiple of 16
 struct MiTokens {
     int e, n0, cols;
@@ -280,10 +226,10 @@ __device__ __forceinline__ void mi_store16(const MiArgs& a, const int32_t (&v)[1
     }
 }
 
-template <int BN, bool SPLIT, bool COPY, bool PAIR>
-__global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS : 0), 1)
+template <int BN, bool SPLIT, bool PAIR>
+__global__ void __launch_bounds__(MI_THREADS, 1)
     matmul_i8_kernel(const __grid_constant__ MiArgs a) {
-    static_assert(!(PAIR && (SPLIT || COPY)), "a pair has one tile at a time and TMA operands");
+    static_assert(!(PAIR && SPLIT), "a pair has a tile's whole K");
     constexpr int XB = mi_box_rows(BN), XROWS = PAIR ? BN / 2 : BN;  // token rows of a box, of this block's stage
     constexpr int STAGE = MI_W_BYTES + XROWS * MI_BK;
     constexpr int TM = PAIR ? 2 * MI_BM : MI_BM;  // channels of a tile
@@ -310,15 +256,15 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
 
     if (tid == 0) {
         for (int s = 0; s < S; s++) {
-            mi_bar_init(&full[s], 1 + (COPY ? 128 : 0));
+            mi_bar_init(&full[s], 1);
             mi_bar_init(&empty[s], 1);
         }
         for (int s = 0; s < 2; s++) {
             mi_bar_init(&accfull[s], 1);
-            mi_bar_init(&accempty[s], PAIR ? 8 : 4);  // a warp of the epilogue each
+            mi_bar_init(&accempty[s], (PAIR ? 2 : 1) * MI_EPI_WARPS);  // a warp of the epilogue each
         }
         mi_bar_init(&fin, 1);
-        mi_bar_init(&redfull, SPLIT ? max(1, 4 * ((int)csize - 1)) : 1);
+        mi_bar_init(&redfull, SPLIT ? max(1, MI_EPI_WARPS * ((int)csize - 1)) : 1);
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -415,7 +361,7 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
             // PAIR: half of the MMA's columns each, and both blocks' bytes awaited by the issuing block
             const int half = PAIR ? mi_columns<PAIR>(tk.cols) >> 1 : 0;
             const int boxes = ((PAIR ? half : tk.cols) + XB - 1) / XB, xrow = tk.n0 + (PAIR ? (int)crank * half : 0);
-            const uint32_t bytes = (COPY && a.copy_w ? 0 : MI_W_BYTES) + (COPY && a.copy_x ? 0 : boxes * XB * MI_BK);
+            const uint32_t bytes = MI_W_BYTES + boxes * XB * MI_BK;
             const int wrow = tk.e * a.M + m * TM + wlead;
             for (int kt = kt0; kt < kt1; kt++) {
                 if (!mi_wait_warp(empty0 + 8 * s, ph, &s_abort, err)) {
@@ -428,13 +374,11 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(full0 + 8 * s),
                                      "r"(PAIR ? 2 * bytes : bytes)
                                      : "memory");
-                    if (!COPY || !a.copy_w) mi_tma<PAIR>(dst, &a.tw, kt * MI_BK, wrow, fb);
-                    if (!COPY || !a.copy_x) {
+                    mi_tma<PAIR>(dst, &a.tw, kt * MI_BK, wrow, fb);
 #pragma unroll
-                        for (int b = 0; b < XROWS / XB; b++)
-                            if (b < boxes)
-                                mi_tma<PAIR>(dst + MI_W_BYTES + b * XB * MI_BK, &a.tx, kt * MI_BK, xrow + b * XB, fb);
-                    }
+                    for (int b = 0; b < XROWS / XB; b++)
+                        if (b < boxes)
+                            mi_tma<PAIR>(dst + MI_W_BYTES + b * XB * MI_BK, &a.tx, kt * MI_BK, xrow + b * XB, fb);
                 }
                 issued++;
                 if (++s == (uint32_t)S) s = 0, ph ^= 1;
@@ -443,12 +387,12 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
             if (m >= a.mt) m -= a.mt, u++;
         }
         if (!ok && lead) {
-            if (!COPY && !PAIR) {
+            if (!PAIR) {
                 // every copy that was issued lands before the block ends
                 for (uint32_t i = issued > (uint32_t)S ? issued - S : 0; i < issued; i++)
                     mi_drain(full0 + 8 * (i % S), (i / S) & 1u);
             } else {
-                // (other warps' arrivals may be missing, so that the phases never complete: time has to do)
+                // (the other block's part may be missing, so that the phases never complete: time has to do)
                 for (int i = 0; i < 64; i++) __nanosleep(1000000);
             }
         }
@@ -494,9 +438,10 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
             mi_drain(mi_smem(&fin), 0);
         }
         __syncwarp();
-    } else if (warp >= 2 && warp < 6) {
-        // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31 ----
-        const int qd = warp & 3;
+    } else if (warp >= 2) {
+        // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31; the two warps of the same lanes take every
+        // other chunk of 16 columns, the next one's load in flight while one is stored ----
+        const int qd = warp & 3, part = (warp - 2) >> 2;
         uint32_t tc = 0;
         for (int u = u0, m = mm0; u < total_u; tc++) {
             const MiTokens tk = mi_tokens(first, tiles, a.E, u);
@@ -516,17 +461,25 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
                     mi_store16<__nv_bfloat16>(a, v, (int64_t)tk.n0 + c0, cols, row, ws, live, lane);
             };
             if (!SPLIT) {
-#pragma unroll 1
-                for (int c0 = 0; c0 < tk.cols; c0 += 16) {
-                    int32_t v[16];
+                int32_t v[16], nx[16];
+                int c0 = 16 * part;
+                if (c0 < tk.cols) {
                     mi_ld16(base + (uint32_t)c0, v);
                     mi_ld_wait();
+                }
+#pragma unroll 1
+                for (; c0 < tk.cols; c0 += 32) {
+                    if (c0 + 32 < tk.cols) mi_ld16(base + (uint32_t)(c0 + 32), nx);
                     put(v, c0, min(16, tk.cols - c0));
+                    mi_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; i++) v[i] = nx[i];
                 }
             } else {
-                // send: columns [d per, (d + 1) per) to block d, at [this block][column][lane]
+                // send: columns [d per, (d + 1) per) to block d, at [this block][column][lane]; the two warps of
+                // the same lanes take every other block
                 const int per = a.per, mrow = 32 * qd + lane;
-                for (uint32_t d = 0; d < csize; d++) {
+                for (uint32_t d = (uint32_t)part; d < csize; d += 2) {
                     if (d == crank) continue;
                     const int lo = (int)d * per, hi = min(tk.cols, lo + per);
                     uint32_t at;
@@ -545,31 +498,29 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    for (uint32_t d = 0; d < csize; d++) {
+                    for (uint32_t d = 0; d < csize; d++)
                         if (d != crank) mi_arrive_at(mi_smem(&redfull), d);
-                    }
                 }
                 __syncwarp();
                 const bool got =
                     csize == 1 || __all_sync(0xffffffffu, mi_wait_scope<true>(mi_smem(&redfull), 0, &s_abort, err));
                 if (!got) break;
                 const int lo = (int)crank * per, hi = min(tk.cols, lo + per);
-                for (int c0 = lo; c0 < hi; c0 += 16) {
-                    // (per is a multiple of 8: a share's last 16 columns may be 8 of the next one's, not stored)
+                for (int c0 = lo + 8 * part; c0 < hi; c0 += 16) {
                     int32_t v[16];
-                    mi_ld16(base + (uint32_t)min(c0, BN - 16), v);
-                    mi_ld_wait();
-                    const int shift = c0 - min(c0, BN - 16);  // 0, or 8 at the accumulator's end
-                    if (shift) {
+                    {
+                        int32_t own[8];
+                        mi_ld8(base + (uint32_t)c0, own);
+                        mi_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 8; i++) v[i] = v[i + 8];
+                        for (int i = 0; i < 8; i++) v[i] = own[i], v[8 + i] = 0;
                     }
-                    const int cols = min(16, hi - c0);
+                    const int cols = min(8, hi - c0);
                     for (uint32_t b = 0; b < csize; b++) {
                         if (b == crank) continue;
                         const int32_t* src = red + ((size_t)b * per + (c0 - lo)) * MI_BM + mrow;
 #pragma unroll
-                        for (int i = 0; i < 16; i++)
+                        for (int i = 0; i < 8; i++)
                             if (i < cols) v[i] += src[i * MI_BM];
                     }
                     put(v, c0, cols);
@@ -582,37 +533,6 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
                     mi_arrive_at(mi_smem(&accempty[slot]), 0);
                 else
                     mi_arrive(mi_smem(&accempty[slot]));
-            }
-            u += du, m += dm;
-            if (m >= a.mt) m -= a.mt, u++;
-        }
-    } else if (COPY && warp >= 6) {
-        // ---- operands that TMA cannot read: group g of four warps fills every MI_COPY_GROUPS-th k-tile ----
-        const int g = (warp - 6) >> 2, t = tid - MI_BASE_THREADS - 128 * g;
-        int s = 0, turn = 0;
-        uint32_t ph = 1;
-        bool ok = true;
-        for (int u = u0, m = mm0; u < total_u && ok;) {
-            const MiTokens tk = mi_tokens(first, tiles, a.E, u);
-            const int rows16 = mi_columns<false>(tk.cols);
-            for (int kt = kt0; kt < kt1; kt++) {
-                if (turn == g) {
-                    if (!mi_wait_warp(mi_smem(&empty[s]), ph, &s_abort, err)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* dst = ring + s * STAGE;
-                    if (a.copy_w)
-                        mi_copy_tile(a.w, a.ldw, (int64_t)a.E * a.M, (int64_t)tk.e * a.M + (int64_t)m * MI_BM, MI_BM,
-                                     (int64_t)(tk.e + 1) * a.M, kt * MI_BK, a.K, dst, t);
-                    if (a.copy_x)
-                        mi_copy_tile(a.x, a.ldx, a.N, tk.n0, rows16, (int64_t)tk.n0 + tk.cols, kt * MI_BK, a.K,
-                                     dst + MI_W_BYTES, t);
-                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // generic writes -> MMA reads
-                    mi_arrive(mi_smem(&full[s]));
-                }
-                if (++turn == MI_COPY_GROUPS) turn = 0;
-                if (++s == S) s = 0, ph ^= 1;
             }
             u += du, m += dm;
             if (m >= a.mt) m -= a.mt, u++;
@@ -632,21 +552,119 @@ __global__ void __launch_bounds__(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS
     }
 }
 
-template <int BN, bool SPLIT, bool COPY, bool PAIR>
-int launch_mi(fp_ctx* c, MiArgs& a, int64_t token_tiles, int split, cudaStream_t st) {
+// ---- operands that TMA cannot read ----------------------------------------------------------
+//
+// TMA wants an address and a pitch that are multiples of 16. Rows that are not so are first copied to rows
+// that are, in stream-ordered memory from the context's pool (inside a graph its own allocation nodes), by
+// one pass: a thread loads the two aligned 16 bytes that its own lie in and shifts. An expert without tokens is
+// passed over. (Realigning inside the product, with warps that
+// load words into the swizzled stages, took 1224 us on 2352 x 9600 x 7454: every tile of channels did the
+// tokens' rows again.)
+
+struct MiOperand {
+    const int8_t* p;
+    int64_t ld, rows;
+};
+
+// rows of K bytes at src (pitch ld) to dst (pitch 16 chunks); the last bytes of a pitch are 0. One thread per
+// 16 bytes, MI_RE of them a block's width apart. M: rows of an expert, with offsets.
+constexpr int MI_RE = 4;
+__global__ void __launch_bounds__(256)
+    realign_rows_kernel(const int8_t* __restrict__ src, int64_t ld, int64_t rows, int K, int8_t* __restrict__ dst,
+                        int chunks, const int32_t* __restrict__ offsets, int M) {
+    const int64_t at0 = (int64_t)blockIdx.x * (256 * MI_RE);
+    const int64_t row0 = at0 / chunks;
+    const int c0 = (int)(at0 % chunks);
+    const FpSpan span = fp_span(src, rows, ld, K);
+#pragma unroll
+    for (int u = 0; u < MI_RE; u++) {
+        const uint32_t i = (uint32_t)c0 + threadIdx.x + 256 * u;
+        const int64_t row = row0 + i / (uint32_t)chunks;
+        const int c = (int)(i % (uint32_t)chunks);
+        if (row >= rows) break;
+        if (offsets) {
+            const int e = (int)(row / M);
+            if (__ldg(offsets + e + 1) <= max(0, __ldg(offsets + e))) continue;
+        }
+        const int8_t* p = src + row * ld + 16 * (int64_t)c;
+        const int valid = K - 16 * c;
+        FpWords<16> w;
+        uint32_t o[4];
+        if (fp_load16_any(p, span, o)) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int left = valid - 4 * j;
+                w.w[j] = o[j] & (left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                w.w[j] = 0;
+#pragma unroll
+                for (int b = 0; b < 4; b++)
+                    if (4 * j + b < valid) w.w[j] |= (uint32_t)(uint8_t)p[4 * j + b] << (8 * b);
+            }
+        }
+        w.store(dst + (row * chunks + c) * 16);
+    }
+}
+
+// Scratch rows of a call, given back to the pool in the order of the stream when the call has queued its work
+struct MiScratch {
+    cudaStream_t st;
+    int8_t* p[2] = {nullptr, nullptr};
+    explicit MiScratch(cudaStream_t s) : st(s) {}
+    ~MiScratch() {
+        for (int8_t* q : p)
+            if (q) cudaFreeAsync(q, st);
+    }
+    MiScratch(const MiScratch&) = delete;
+    MiScratch& operator=(const MiScratch&) = delete;
+};
+
+// makes the operand readable for TMA
+int mi_realign(fp_ctx* c, MiOperand& o, int K, const int32_t* offsets, int M, int8_t** scratch, cudaStream_t st) {
+    if (((uintptr_t)o.p | (uint64_t)o.ld) % 16 == 0) return FP_OK;
+    const int64_t dld = (K + 15) & ~15;
+    if (!c->pool) return fp_fail(c, FP_ERR_OOM, "fp_matmul_i8: no memory pool for realigned rows on this device");
+    const cudaError_t e = cudaMallocFromPoolAsync((void**)scratch, (size_t)dld * o.rows, c->pool, st);
+    if (e != cudaSuccess) {
+        *scratch = nullptr;
+        cudaGetLastError();
+        return fp_fail(c, FP_ERR_OOM, std::string("fp_matmul_i8: ") + std::to_string((size_t)dld * o.rows) +
+                                          " bytes for realigned rows: " + cudaGetErrorString(e));
+    }
+    const int chunks = (int)(dld / 16);
+    const int64_t blocks = (o.rows * chunks + 256 * MI_RE - 1) / (256 * MI_RE);
+    if (blocks > 0x7fffffffll) return fp_fail(c, FP_ERR_SHAPE, "fp_matmul_i8: an operand of over 2^45 bytes with an odd pitch");
+    int slot;
+    fp_op_tic(c, st, K_REALIGN, 2.0 * (double)K * o.rows, &slot);
+    realign_rows_kernel<<<(unsigned)blocks, 256, 0, st>>>(o.p, o.ld, o.rows, K, *scratch, chunks, offsets, M);
+    fp_toc(c, st, slot);
+    FP_CUDA(c, cudaGetLastError());
+    o.p = *scratch;
+    o.ld = dld;
+    return FP_OK;
+}
+
+template <int BN, bool SPLIT, bool PAIR>
+int launch_mi(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x, int64_t token_tiles, int split, cudaStream_t st) {
     constexpr int STAGE = MI_W_BYTES + (PAIR ? BN / 2 : BN) * MI_BK;
     constexpr int TM = PAIR ? 2 * MI_BM : MI_BM;
     const int cluster = PAIR ? 2 : split;
+    if (!fp_tmap_u8_2d(&a.tw, w.p, (uint64_t)a.K, (uint64_t)w.rows, (uint64_t)w.ld, MI_BK, MI_BM, true) ||
+        !fp_tmap_u8_2d(&a.tx, x.p, (uint64_t)a.K, (uint64_t)x.rows, (uint64_t)x.ld, MI_BK, mi_box_rows(BN), true))
+        return fp_fail(c, FP_ERR_CUDA, "fp_matmul_i8: tensor map encoding failed");
     a.mt = (a.M + TM - 1) / TM;
     a.per = SPLIT ? (((BN + split - 1) / split) + 7) & ~7 : 0;
     const size_t extra = (SPLIT ? (size_t)split * a.per * MI_BM * 4 : 0) + 8 * ((size_t)a.E + 1) + 1024;
     a.stages = (int)std::min<size_t>(MI_MAX_STAGES, (MI_SMEM - extra) / STAGE);
-    auto kern = matmul_i8_kernel<BN, SPLIT, COPY, PAIR>;
-    FP_CUDA(c, fp_op_smem(c, 1 + (BN == 32 ? 0 : BN == 128 ? 8 : 16) + 4 * SPLIT + 2 * COPY + PAIR, kern, MI_SMEM));
+    auto kern = matmul_i8_kernel<BN, SPLIT, PAIR>;
+    FP_CUDA(c, fp_op_smem(c, 1 + (BN == 32 ? 0 : BN == 128 ? 4 : 8) + 2 * SPLIT + PAIR, kern, MI_SMEM));
     const int64_t tiles = token_tiles * a.mt;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(cluster * (SPLIT ? tiles : std::min<int64_t>(tiles, c->num_sms / cluster))));
-    cfg.blockDim = dim3(MI_BASE_THREADS + (COPY ? 128 * MI_COPY_GROUPS : 0));
+    cfg.blockDim = dim3(MI_THREADS);
     cfg.dynamicSmemBytes = a.stages * STAGE + extra;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -659,38 +677,24 @@ int launch_mi(fp_ctx* c, MiArgs& a, int64_t token_tiles, int split, cudaStream_t
     return FP_OK;
 }
 
-// operands whose rows TMA can address (the others are copied by warps); true if both are
-bool mi_maps(MiArgs& a, int bn) {
-    a.copy_w = ((uintptr_t)a.w | (uint64_t)a.ldw) % 16 != 0 ||
-               !fp_tmap_u8_2d(&a.tw, a.w, (uint64_t)a.K, (uint64_t)a.E * a.M, (uint64_t)a.ldw, MI_BK, MI_BM, true);
-    a.copy_x = ((uintptr_t)a.x | (uint64_t)a.ldx) % 16 != 0 ||
-               !fp_tmap_u8_2d(&a.tx, a.x, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.ldx, MI_BK, mi_box_rows(bn), true);
-    return !a.copy_w && !a.copy_x;
-}
-
 // token tiles at most: every group that can have rows has one, and the rows fill the others
 int64_t mi_token_tiles(const MiArgs& a, int bn) {
     const int64_t groups = std::min(a.E, a.N);
     return groups == 1 ? (a.N + bn - 1) / bn : groups + a.N / bn;
 }
 
-int launch_split_or_not(fp_ctx* c, MiArgs& a, int64_t rows, cudaStream_t st) {
-    // a group of more than 32 rows fills wider tiles
+int launch_product(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x, int64_t rows, cudaStream_t st) {
+    const int64_t mt = (a.M + MI_BM - 1) / MI_BM, nk = (a.K + MI_BK - 1) / MI_BK;
+    a.nk = (int32_t)nk;
     const int bn = rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
-    const int64_t tiles = mi_token_tiles(a, bn) * ((a.M + MI_BM - 1) / MI_BM);
-    const bool tma = mi_maps(a, bn);
-    int split = 1;
-    while (bn <= 128 && split < 8 && tiles * split * 2 <= c->num_sms && split * 4 <= a.nk) split *= 2;
     const int64_t tt = mi_token_tiles(a, bn);
-    if (bn == 32) {
-        if (split > 1) return tma ? launch_mi<32, true, false, false>(c, a, tt, split, st) : launch_mi<32, true, true, false>(c, a, tt, split, st);
-        return tma ? launch_mi<32, false, false, false>(c, a, tt, 1, st) : launch_mi<32, false, true, false>(c, a, tt, 1, st);
-    }
-    if (split > 1) return tma ? launch_mi<128, true, false, false>(c, a, tt, split, st) : launch_mi<128, true, true, false>(c, a, tt, split, st);
-    // wider tiles: pairs of blocks, or one block that copies
-    const int64_t wide = mi_token_tiles(a, 256);
-    if (mi_maps(a, 256)) return launch_mi<256, false, false, true>(c, a, wide, 1, st);
-    return launch_mi<256, false, true, false>(c, a, wide, 1, st);
+    int split = 1;
+    while (bn <= 128 && split < 8 && tt * mt * split * 2 <= c->num_sms && split * 4 <= nk) split *= 2;
+    if (bn == 32)
+        return split > 1 ? launch_mi<32, true, false>(c, a, w, x, tt, split, st)
+                         : launch_mi<32, false, false>(c, a, w, x, tt, 1, st);
+    if (split > 1) return launch_mi<128, true, false>(c, a, w, x, tt, split, st);
+    return launch_mi<256, false, true>(c, a, w, x, mi_token_tiles(a, 256), 1, st);
 }
 
 }  // namespace
@@ -722,17 +726,20 @@ int fp_matmul_i8(fp_ctx* c, const int8_t* w, int64_t ldw, const float* w_scale, 
     cudaStream_t st = (cudaStream_t)stream;
     if (N == 1) ldx = (K + 15) & ~15ll, ldy = M;  // a single row has no pitch: one that keeps its alignment
     if (E * M == 1) ldw = (K + 15) & ~15ll;
+    MiOperand ow{w, ldw, E * M}, ox{x, ldx, N};
+    MiScratch scratch(st);
+    int rc = mi_realign(c, ow, (int)K, E > 1 ? offsets : nullptr, (int)M, &scratch.p[0], st);
+    if (!rc) rc = mi_realign(c, ox, (int)K, nullptr, 1, &scratch.p[1], st);
+    if (rc) return rc;
     MiArgs a = {};
-    a.w = w, a.w_scale = w_scale, a.x = x, a.x_scale = x_scale, a.offsets = offsets, a.y = y;
-    a.ldw = ldw, a.ldx = ldx, a.ldy = ldy;
+    a.w_scale = w_scale, a.x_scale = x_scale, a.offsets = offsets, a.y = y, a.ldy = ldy;
     a.M = (int32_t)M, a.K = (int32_t)K, a.N = (int32_t)N, a.E = E, a.y_type = y_type;
-    a.nk = (int32_t)((K + MI_BK - 1) / MI_BK);
     a.err = &c->mb_dev->op_err;
     // rows of a group: N of a dense product, twice the mean of those that can have rows by expert
     const int64_t rows = E == 1 ? N : 2 * ((N + std::min<int64_t>(E, N) - 1) / std::min<int64_t>(E, N));
     int slot;
     fp_op_tic(c, st, K_MATMUL_I8, (double)std::min<int64_t>(E, N) * M * K + (double)N * (K + ys * (double)M), &slot);
-    const int rc = launch_split_or_not(c, a, rows, st);
+    rc = launch_product(c, a, ow, ox, rows, st);
     fp_toc(c, st, slot);
     return rc;
 }

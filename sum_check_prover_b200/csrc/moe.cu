@@ -150,20 +150,26 @@ __global__ void __launch_bounds__(1024)
 constexpr int MO_CHOICES = 4;  // positions (and weights) of a token kept in registers at a time
 
 // rows[pos[t][j]] = x[t] in units of A bytes; one token per tpr threads, blockIdx.y a share of the columns. U
-// loads of a thread are in flight before its stores.
-template <int A, int U>
+// loads of a thread are in flight before its stores. ANY: x from any address.
+template <int A, int U, bool ANY>
 __global__ void __launch_bounds__(FP_ROW_THREADS)
     moe_dispatch_kernel(const char* __restrict__ x, int64_t T, int nvec, int64_t ldx, const int32_t* __restrict__ pos,
                         int k, int64_t R, char* __restrict__ rows, int64_t ldr, int tpr) {
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
     const char* src = x + t * ldx;
+    const FpSpan span = fp_span(x, T, ldx, (int64_t)nvec * A);
     const int step = tpr * gridDim.y;
     for (int c = threadIdx.x % tpr + tpr * blockIdx.y; c < nvec; c += U * step) {
         FpWords<A> v[U];
 #pragma unroll
         for (int u = 0; u < U; u++)
-            if (c + u * step < nvec) v[u].load(src + (int64_t)(c + u * step) * A);
+            if (c + u * step < nvec) {
+                if constexpr (ANY)
+                    v[u].template load_any<1>(src + (int64_t)(c + u * step) * A, span);
+                else
+                    v[u].load(src + (int64_t)(c + u * step) * A);
+            }
         for (int j0 = 0; j0 < k; j0 += MO_CHOICES) {
             char* dst[MO_CHOICES];
 #pragma unroll
@@ -182,21 +188,21 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
     }
 }
 
-template <int A>
+template <int A, bool ANY>
 void launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, int64_t ldx, const int32_t* pos, int k,
                      int64_t R, void* rows, int64_t ldr, cudaStream_t st) {
     const int nvec = (int)(bytes / A);
     constexpr int U = A == 16 ? 2 : 4;
     const FpRowGrid g = fp_row_grid(c, T, nvec, U, true);
-    moe_dispatch_kernel<A, U><<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const char*)x, T, nvec, ldx, pos, k, R,
+    moe_dispatch_kernel<A, U, ANY><<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const char*)x, T, nvec, ldx, pos, k, R,
                                                                         (char*)rows, ldr, g.tpr);
 }
 
 // ---- combine --------------------------------------------------------------------------------
 
-// out[t] = base[t] + sum_j w[t][j] rows[pos[t][j]] in fp32, rounded once; V elements per load, U vectors
-// of a thread at a time
-template <typename RT, typename OT, int V, int U>
+// out[t] = base[t] + sum_j w[t][j] rows[pos[t][j]] in fp32, rounded once; V elements per load (ANY: from any
+// address), U vectors of a thread at a time
+template <typename RT, typename OT, int V, int U, bool ANY>
 __global__ void __launch_bounds__(FP_ROW_THREADS)
     moe_combine_kernel(const RT* __restrict__ rows, int64_t R, int64_t ldr, const int32_t* __restrict__ pos,
                        const float* __restrict__ w, const OT* base, int64_t ldb, int64_t T, int k, int nvec, OT* out,
@@ -204,13 +210,14 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
     const int step = tpr * gridDim.y;
+    const FpSpan span = fp_span(rows, R, ldr, (int64_t)nvec * V);
     for (int c = threadIdx.x % tpr + tpr * blockIdx.y; c < nvec; c += U * step) {
         float acc[U][V];
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const bool in = base && c + u * step < nvec;
             FpVec<OT, V> b;
-            if (in) b.load(base + t * ldb + (int64_t)(c + u * step) * V);
+            if (in) b.template load_row<ANY>(base + t * ldb + (int64_t)(c + u * step) * V, fp_span(base, T, ldb, (int64_t)nvec * V));
 #pragma unroll
             for (int i = 0; i < V; i++) acc[u][i] = in ? b.get(i) : 0.0f;
         }
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
             for (int j = 0; j < 2; j++)
 #pragma unroll
                 for (int u = 0; u < U; u++)
-                    if (src[j] && c + u * step < nvec) v[j][u].load(src[j] + (int64_t)(c + u * step) * V);
+                    if (src[j] && c + u * step < nvec) v[j][u].template load_row<ANY>(src[j] + (int64_t)(c + u * step) * V, span);
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 if (!src[j]) continue;
@@ -251,19 +258,23 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
 
 // ---- gradients of combine -------------------------------------------------------------------
 
+constexpr int MO_GRAD_THREADS = 512;
+
 // One token per tpr threads: its k rows' gradients and the k inner products (fp32, a fixed order: a
-// thread's columns, its warp's tree, then the warps). Two choices at a time read dout once.
-template <typename RT, typename OT, int V, int U>
-__global__ void __launch_bounds__(FP_ROW_THREADS)
+// thread's columns, its warp's tree, then the warps). Two choices at a time read dout once; blockIdx.y a
+// share of the choices. ANY: loads from any address.
+template <typename RT, typename OT, int V, int U, bool ANY>
+__global__ void __launch_bounds__(MO_GRAD_THREADS)
     moe_grad_kernel(const OT* __restrict__ dout, int64_t ldd, const RT* __restrict__ rows, int64_t R, int64_t ldr,
                     const int32_t* __restrict__ pos, const float* __restrict__ w, int64_t T, int k, int nvec,
-                    RT* __restrict__ drows, int64_t lddr, float* __restrict__ dw, int tpr) {
+                    RT* __restrict__ drows, int64_t lddr, float* __restrict__ dw, int tpr, bool dvec) {
     __shared__ float red[2][32];
     const int sub = threadIdx.x / tpr, tt = threadIdx.x % tpr, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + sub;
     const bool live = t < T;
     const OT* g = dout + (live ? t : 0) * ldd;
-    for (int j0 = 0; j0 < k; j0 += 2) {
+    const FpSpan gspan = fp_span(dout, T, ldd, (int64_t)nvec * V), rspan = fp_span(rows, R, ldr, (int64_t)nvec * V);
+    for (int j0 = 2 * blockIdx.y; j0 < k; j0 += 2 * gridDim.y) {
         int64_t p[2];
         float s[2], dot[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -277,13 +288,14 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
             FpVec<RT, V> v[2][U];
 #pragma unroll
             for (int u = 0; u < U; u++)
-                if (c + u * tpr < nvec) gv[u].load(g + (int64_t)(c + u * tpr) * V);
+                if (c + u * tpr < nvec) gv[u].template load_row<ANY>(g + (int64_t)(c + u * tpr) * V, gspan);
             if (dw) {
 #pragma unroll
                 for (int j = 0; j < 2; j++)
 #pragma unroll
                     for (int u = 0; u < U; u++)
-                        if (p[j] >= 0 && c + u * tpr < nvec) v[j][u].load(rows + p[j] * ldr + (int64_t)(c + u * tpr) * V);
+                        if (p[j] >= 0 && c + u * tpr < nvec)
+                            v[j][u].template load_row<ANY>(rows + p[j] * ldr + (int64_t)(c + u * tpr) * V, rspan);
             }
 #pragma unroll
             for (int j = 0; j < 2; j++) {
@@ -301,7 +313,13 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
                         for (int i = 0; i < V; i++) f[i] = s[j] * gv[u].get(i);
                         FpVec<RT, V> o;
                         o.set(f);
-                        o.store(drows + p[j] * lddr + (int64_t)(c + u * tpr) * V);
+                        RT* d = drows + p[j] * lddr + (int64_t)(c + u * tpr) * V;
+                        if (dvec) {
+                            o.store(d);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < V; i++) d[i] = fp_from_f<RT>(f[i]);
+                        }
                     }
                 }
             }
@@ -313,7 +331,7 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
                 for (int m = 16; m > 0; m >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], m);
             float sum = lane ? dot[1] : dot[0];
             if (tpr > 32) {
-                if (j0) __syncthreads();  // red may still be read for the choices before
+                if (j0 > 2 * (int)blockIdx.y) __syncthreads();  // red may still be read for the choices before
                 if (lane < 2) red[lane][warp] = sum;
                 __syncthreads();
                 if (tt < 2) {
@@ -357,12 +375,16 @@ int fp_moe_sort(fp_ctx* c, const int32_t* e, int64_t n, int E, int32_t* offsets,
     FpDeviceScope dev(c);
     if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_moe_sort");
     cudaStream_t st = (cudaStream_t)stream;
-    // as many warps as have 32 choices each: one block, then a cluster of up to eight
-    const int64_t need = std::max<int64_t>(1, (n + 31) / 32);
+    // One block below 1024 choices, a cluster of eight from there (1024 choices of 128 experts: 4.9 and 4.4 us;
+    // 256: 3.7 and 4.1). A block's warps cost time in the sums over them, their rounds of 32 choices in the
+    // ranking: about sqrt(2 rounds) warps (8192 choices: 4, 8, 16, 32 warps take 6.9, 5.6, 5.7, 6.7 us), more
+    // where that keeps the choices in registers.
+    const int64_t rounds = std::max<int64_t>(1, (n + 31) / 32);
     const int most = (int)std::min<int64_t>(32, MS_HIST_BYTES / (4 * (int64_t)E));
-    int blocks = 1;
-    while (blocks < MS_MAX_CLUSTER && need > (int64_t)blocks * most) blocks *= 2;
-    const int warps = (int)std::min<int64_t>(most, (need + blocks - 1) / blocks);
+    const int blocks = rounds >= 32 ? MS_MAX_CLUSTER : 1;
+    const int64_t per = (rounds + blocks - 1) / blocks;
+    int warps = 1;
+    while (warps < most && ((int64_t)warps * warps < 2 * per || (int64_t)warps * MS_KEEP < per)) warps++;
     const int threads = std::max(32 * warps, 128);
     const size_t smem = sizeof(int32_t) * ((size_t)warps * E + 2 * (size_t)E);
     FP_CUDA(c, fp_op_smem(c, 0, moe_sort_kernel, MS_HIST_BYTES + 8 * 4096));
@@ -407,15 +429,17 @@ int fp_moe_dispatch(fp_ctx* c, const void* x, int64_t T, int64_t row_bytes, int6
     int slot;
     fp_op_tic(c, st, K_MOE_DISPATCH, (double)row_bytes * (T + T * (double)k) + 4.0 * T * k, &slot);
     if (al >= 16)
-        launch_dispatch<16>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<16, false>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+    else if (fp_common_align({(uint64_t)(uintptr_t)rows, (uint64_t)ldr, (uint64_t)row_bytes}) >= 16)
+        launch_dispatch<16, true>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 8)
-        launch_dispatch<8>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<8, false>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 4)
-        launch_dispatch<4>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<4, false>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 2)
-        launch_dispatch<2>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<2, false>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else
-        launch_dispatch<1>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<1, false>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     fp_toc(c, st, slot);
     FP_CUDA(c, cudaGetLastError());
     return FP_OK;
@@ -450,19 +474,23 @@ int fp_moe_combine(fp_ctx* c, const void* rows, int rows_type, int64_t R, int64_
         by_type(out_type, [&](auto* op) {
             using OT = std::remove_pointer_t<decltype(op)>;
             constexpr int V = 16 / sizeof(RT), OA = V * sizeof(OT) < 16 ? V * sizeof(OT) : 16;
-            const bool vec = M % V == 0 && fp_common_align({(uint64_t)(uintptr_t)rows, (uint64_t)ldr * rs}) == 16 &&
-                             fp_common_align({(uint64_t)(uintptr_t)out, (uint64_t)(uintptr_t)base, (uint64_t)ldo * os,
-                                              (uint64_t)ldb * os}) >= OA;
+            const bool vec = M % V == 0 && fp_common_align({(uint64_t)(uintptr_t)out, (uint64_t)ldo * os}) >= OA;
+            const bool aligned = fp_common_align({(uint64_t)(uintptr_t)rows, (uint64_t)ldr * rs}) == 16 &&
+                                 fp_common_align({(uint64_t)(uintptr_t)base, (uint64_t)ldb * os}) >= OA;
             const int nvec = (int)(vec ? M / V : M);
             auto run = [&](auto kern, int loads) {
                 const FpRowGrid g = fp_row_grid(c, T, nvec, loads, true);
                 kern<<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const RT*)rows, R, ldr, pos, weights, (const OT*)base, ldb, T,
                                                                k, nvec, (OT*)out, ldo, g.tpr);
             };
-            if (vec)  // two loads in flight either way: of two choices, or of two vectors
-                k > 1 ? run(moe_combine_kernel<RT, OT, V, 1>, 1) : run(moe_combine_kernel<RT, OT, V, 2>, 2);
+            if (!vec)
+                run(moe_combine_kernel<RT, OT, 1, 4, false>, 4);
+            else if (!aligned)
+                run(moe_combine_kernel<RT, OT, V, 1, true>, 1);
+            else if (k <= 2)  // (8192 x 5120, k = 2: 43.2 and 43.9 us with one vector and two; 1024, k = 8: 22.9 and 19.5)
+                run(moe_combine_kernel<RT, OT, V, 1, false>, 1);
             else
-                run(moe_combine_kernel<RT, OT, 1, 4>, 4);
+                run(moe_combine_kernel<RT, OT, V, 2, false>, 2);
         });
     });
     fp_toc(c, st, slot);
@@ -503,17 +531,26 @@ int fp_moe_combine_grad(fp_ctx* c, const void* dout, int out_type, int64_t ldd, 
         by_type(out_type, [&](auto* op) {
             using OT = std::remove_pointer_t<decltype(op)>;
             constexpr int V = 16 / sizeof(RT), OA = V * sizeof(OT) < 16 ? V * sizeof(OT) : 16;
-            const bool vec = M % V == 0 &&
-                             fp_common_align({(uint64_t)(uintptr_t)rd, (uint64_t)(uintptr_t)drows, (uint64_t)ldr * rs,
-                                              (uint64_t)lddr * rs}) == 16 &&
-                             fp_common_align({(uint64_t)(uintptr_t)dout, (uint64_t)ldd * os}) >= OA;
+            // (by M alone, so that dweights' order of summation does not hang on what else is asked for)
+            const bool vec = M % V == 0, dvec = fp_common_align({(uint64_t)(uintptr_t)drows, (uint64_t)lddr * rs}) == 16;
+            const bool aligned = fp_common_align({(uint64_t)(uintptr_t)rd, (uint64_t)ldr * rs}) == 16 &&
+                                 fp_common_align({(uint64_t)(uintptr_t)dout, (uint64_t)ldd * os}) >= OA;
             const int nvec = (int)(vec ? M / V : M);
             auto run = [&](auto kern, int loads) {
-                const FpRowGrid g = fp_row_grid(c, T, nvec, loads, false);
-                kern<<<g.gx, g.threads(), 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k, nvec,
-                                                   (RT*)drows, lddr, dweights, g.tpr);
+                FpRowGrid g = fp_row_grid(c, T, nvec, loads, false);
+                if (T * nvec < (int64_t)c->num_sms * 1024) {  // few tokens: wider blocks, the choices over blocks
+                    while (g.tpr < MO_GRAD_THREADS && g.tpr * loads < nvec) g.tpr *= 2;
+                    g.rpb = std::max(1, FP_ROW_THREADS / g.tpr);
+                    g.gx = (unsigned)((T + g.rpb - 1) / g.rpb);
+                    g.gy = (unsigned)std::min(k / 2 + (k & 1), 32);
+                }
+                kern<<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k,
+                                                               nvec, (RT*)drows, lddr, dweights, g.tpr, !vec || dvec);
             };
-            vec ? run(moe_grad_kernel<RT, OT, V, 1>, 1) : run(moe_grad_kernel<RT, OT, 1, 4>, 4);
+            if (!vec)
+                run(moe_grad_kernel<RT, OT, 1, 4, false>, 4);
+            else
+                aligned ? run(moe_grad_kernel<RT, OT, V, 1, false>, 1) : run(moe_grad_kernel<RT, OT, V, 1, true>, 1);
         });
     });
     fp_toc(c, st, slot);

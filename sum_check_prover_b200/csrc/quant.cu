@@ -1,9 +1,12 @@
 // fp_quantize_rows: activations to int8 with one scale a token.
 //
 // a_t = max_j |x_tj|, scale_t = a_t / 127 (fp32), q_tj = the integer nearest to 127 x_tj / a_t, ties to
-// the even one. The integer is exact: a product with the fp32 value of 127 / a_t is off by less than
-// 127 * 2^-23, so only a value within 2^-15 of a half can round to the wrong side, and those compare
-// 254 |x| with (2 n + 1) a_t, products that are exact in fp32 for 16-bit values and in double for others.
+// the even one, exactly. The kernel multiplies by 127 / a_t, rounded up, in fp32: off by less than 127 * 2^-22.
+// A 16-bit value that is not at a half itself is further from one than that: 254 x - (2 n + 1) a_t is a multiple of
+// x's last place, so 127 x / a_t differs from n + 1/2 by 2^-12 / 127 of itself at least. At a half, 254 x = (2 n + 1)
+// a_t, the prime 127 divides 2 n + 1, so that n = 63 and the quotient rounded up goes to 64 as it has to, or it
+// divides a_t: with 8 bits the quotient is then exact, with f16's 11 such rows are done value by value. fp32 values
+// within 2^-15 of a half are done one by one too. One by one: 254 |x| against (2 n + 1) a_t, exact in double.
 //
 // A row with a NaN or an infinity has no scale: its scale is NaN and its integers are 0, so every
 // product with it is NaN. A row of zeros has scale 0.
@@ -20,28 +23,20 @@ constexpr float QR_NEAR = 0.5f - 3.0517578e-5f;
 
 // what a row's values are divided by: 127 / a, and the row scaled by 2^64 where 127 / a may not be finite
 struct QuantRow {
-    float inv;         // of the fast quotient; 0 in a row of zeros, with a NaN or an infinity, or scaled up
+    float inv;            // of the fast quotient; 0 in a row of zeros or with a NaN or an infinity
     float up, a, inv_up;  // 1 or 2^64; a up; 127 / (a up)
-    bool bad;          // integers 0
-    bool tiny;         // scaled up: every value exactly
+    bool bad;             // integers 0
+    bool exact;           // every value by quant_exact
 };
 
 // x's integer as a float: the nearest to t = 127 x / a unless t lies next to a half, then by 254 |x| - (2 n + 1) a
-template <typename T>
 __device__ __forceinline__ float quant_exact(float x, const QuantRow& row) {
     const float ax = fabsf(x) * row.up, t = ax * row.inv_up, r = (t + QR_MAGIC) - QR_MAGIC;
     float n = r;
     if (fabsf(t - r) > QR_NEAR) {
         n = t > r ? r : r - 1.0f;
-        bool above, tie;
-        if constexpr (sizeof(T) == 2) {  // at most 11 + 8 bits: both products are exact
-            const float d = 254.0f * ax - (2.0f * n + 1.0f) * row.a;
-            above = d > 0.0f, tie = d == 0.0f;
-        } else {
-            const double d = 254.0 * (double)ax - (double)(2.0f * n + 1.0f) * (double)row.a;
-            above = d > 0.0, tie = d == 0.0;
-        }
-        if (above || (tie && ((int)n & 1))) n += 1.0f;
+        const double d = 254.0 * (double)ax - (double)(2.0f * n + 1.0f) * (double)row.a;
+        if (d > 0.0 || (d == 0.0 && ((int)n & 1))) n += 1.0f;
     }
     return copysignf(n, x);
 }
@@ -54,11 +49,11 @@ __device__ __forceinline__ FpWords<V> quant_vec(const FpVec<T, V>& w, const Quan
     for (int e = 0; e < V; e++) {
         const float t = w.get(e) * row.inv;
         n[e] = t + QR_MAGIC;
-        off = fmaxf(off, fabsf(t - (n[e] - QR_MAGIC)));
+        if (sizeof(T) == 4) off = fmaxf(off, fabsf(t - (n[e] - QR_MAGIC)));
     }
-    if (off > QR_NEAR || row.tiny) {
+    if (off > QR_NEAR || row.exact) {
 #pragma unroll
-        for (int e = 0; e < V; e++) n[e] = quant_exact<T>(w.get(e), row) + QR_MAGIC;
+        for (int e = 0; e < V; e++) n[e] = quant_exact(w.get(e), row) + QR_MAGIC;
     }
     FpWords<V> o;
     if constexpr (V == 1) {
@@ -88,9 +83,10 @@ __device__ __forceinline__ uint32_t quant_largest(const FpVec<T, V>& w, uint32_t
     return m;
 }
 
-// One row per `tpr` threads (a multiple of 32 that divides the block). V: elements per load; a thread
+// One row per `tpr` threads (a multiple of 32 that divides the block). V: elements per load (ANY: from any
+// address); a thread
 // keeps the first NV vectors it reads in registers, and reads what is beyond them a second time.
-template <typename T, int V, int NV>
+template <typename T, int V, int NV, bool ANY>
 __global__ void __launch_bounds__(256, 4)
     quant_rows_kernel(const T* __restrict__ x, int64_t rows, int K, int64_t ldx, const int32_t* __restrict__ pos, int k,
                       int64_t R, int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale, int tpr, bool qvec) {
@@ -101,11 +97,12 @@ __global__ void __launch_bounds__(256, 4)
     const T* xr = x + (live ? row : 0) * ldx;
     const int nvec = live ? K / V : 0;
     const int64_t p0 = !live ? -1 : pos ? __ldg(pos + row * k) : row;
+    const FpSpan span = fp_span(x, rows, ldx, K);
     FpVec<T, V> reg[NV];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         if (t + i * tpr < nvec) {
-            reg[i].load(xr + (t + i * tpr) * V);
+            reg[i].template load_row<ANY>(xr + (t + i * tpr) * V, span);
         } else {
 #pragma unroll
             for (int e = 0; e < FpVec<T, V>::W; e++) reg[i].w[e] = 0;
@@ -116,7 +113,7 @@ __global__ void __launch_bounds__(256, 4)
     for (int i = 0; i < NV; i++) m = quant_largest<T, V>(reg[i], m);
     for (int c = t + NV * tpr; c < nvec; c += tpr) {
         FpVec<T, V> w;
-        w.load(xr + c * V);
+        w.template load_row<ANY>(xr + c * V, span);
         m = quant_largest<T, V>(w, m);
     }
     if (sizeof(T) == 2) m = max(m >> 16, m & 0xffffu);
@@ -133,11 +130,13 @@ __global__ void __launch_bounds__(256, 4)
     const float amax = top.get(0);
     QuantRow r;
     r.bad = !(amax < __uint_as_float(0x7f800000u));  // an infinity or NaN
-    r.tiny = amax < 5.421010862427522e-20f && m != 0;  // 2^-64
-    r.up = r.tiny ? 18446744073709551616.0f : 1.0f;
+    const bool tiny = amax < 5.421010862427522e-20f && m != 0;  // 2^-64
+    r.up = tiny ? 18446744073709551616.0f : 1.0f;
     r.a = amax * r.up;
-    r.inv_up = r.bad || m == 0 ? 0.0f : 127.0f / r.a;
-    r.inv = r.tiny ? 0.0f : r.inv_up;
+    r.inv_up = r.bad || m == 0 ? 0.0f : __fdiv_ru(127.0f, r.a);
+    r.inv = tiny ? 0.0f : r.inv_up;
+    // f16 rows whose maximum is a multiple of 127 have ties at every half
+    r.exact = tiny || (std::is_same_v<T, __half> && m != 0 && ((m & 0x3ffu) | (m >= 0x400u ? 0x400u : 0u)) % 127u == 0);
     const int copies = pos ? k : 1;
     FpWords<V> o[NV];
 #pragma unroll
@@ -160,7 +159,7 @@ __global__ void __launch_bounds__(256, 4)
             if (t + i * tpr < nvec) put(t + i * tpr, o[i]);
         for (int c = t + NV * tpr; c < nvec; c += tpr) {
             FpVec<T, V> w;
-            w.load(xr + c * V);
+            w.template load_row<ANY>(xr + c * V, span);
             put(c, quant_vec<T, V>(w, r));
         }
     }
@@ -170,8 +169,8 @@ template <typename T>
 void launch_quant(const fp_ctx* c, const void* x, int64_t T_, int64_t K, int64_t ldx, const int32_t* pos, int k,
                   int64_t R, int8_t* q, int64_t ldq, float* scale, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = fp_common_align({(uint64_t)(uintptr_t)x, (uint64_t)ldx * sizeof(T), (uint64_t)K * sizeof(T)}) == 16;
-    const bool qvec = fp_common_align({(uint64_t)(uintptr_t)q, (uint64_t)ldq}) >= V;
+    const bool aligned = fp_common_align({(uint64_t)(uintptr_t)x, (uint64_t)ldx * sizeof(T)}) == 16;
+    const bool vec = K % V == 0, qvec = fp_common_align({(uint64_t)(uintptr_t)q, (uint64_t)ldq}) >= V;
     const int64_t nvec = vec ? K / V : K;
     // a few warps hold a row in registers, so that many rows are in flight; few rows: a vector a thread
     auto run = [&](auto kern, int loads) {
@@ -181,7 +180,10 @@ void launch_quant(const fp_ctx* c, const void* x, int64_t T_, int64_t K, int64_t
         const unsigned grid = (unsigned)((T_ + threads / tpr - 1) / (threads / tpr));
         kern<<<grid, threads, 0, st>>>((const T*)x, T_, (int)K, ldx, pos, k, R, q, ldq, scale, tpr, qvec || !vec);
     };
-    vec ? run(quant_rows_kernel<T, V, QR_LOADS>, QR_LOADS) : run(quant_rows_kernel<T, 1, 2 * QR_LOADS>, 2 * QR_LOADS);
+    if (!vec)
+        run(quant_rows_kernel<T, 1, 2 * QR_LOADS, false>, 2 * QR_LOADS);
+    else
+        aligned ? run(quant_rows_kernel<T, V, QR_LOADS, false>, QR_LOADS) : run(quant_rows_kernel<T, V, QR_LOADS, true>, QR_LOADS);
 }
 
 }  // namespace

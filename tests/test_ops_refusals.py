@@ -175,6 +175,6 @@ def test_moe_checks(fp):
 
 def test_kernels_have_names(fp):
     names = fp.kernel_names()
-    for n in ("quant_rows", "matmul_i8", "moe_sort", "moe_dispatch", "moe_combine", "moe_grad"):
+    for n in ("quant_rows", "matmul_i8", "realign_rows", "moe_sort", "moe_dispatch", "moe_combine", "moe_grad"):
         assert n in names
     assert len(set(names)) == len(names)

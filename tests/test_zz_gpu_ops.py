@@ -84,7 +84,7 @@ TYPES = ["float32", "float16", "bfloat16"]
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,K,pad,lead", [(1, 1, 0, 0), (1, 7, 0, 0), (3, 64, 0, 0), (5, 129, 0, 1), (2, 1024, 16, 0),
                                           (150, 257, 3, 0), (7, 5120, 0, 0), (2, 16384, 8, 0), (3, 40000, 0, 0),
-                                          (2, 33001, 0, 1), (1100, 96, 0, 0)])
+                                          (2, 33001, 0, 1), (1100, 96, 0, 0), (40, 256, 3, 1), (3, 9008, 5, 2)])
 def test_quantize_rows(env, dtype, T, K, pad, lead):
     torch, fp, ctx = env
     dt = getattr(torch, dtype)
@@ -365,7 +365,7 @@ def routed(rng, T, k, E, R=None, drop=0.1):
 
 
 @pytest.mark.parametrize("dtype,K,pad,lead", [("int8", 1, 0, 0), ("int8", 33, 0, 0), ("int8", 64, 0, 0), ("int8", 40, 0, 1), ("bfloat16", 8, 0, 0),
-                                              ("bfloat16", 513, 1, 0), ("float32", 100, 0, 0), ("float32", 5, 3, 1), ("float16", 2048, 8, 0),
+                                              ("bfloat16", 513, 1, 0), ("float32", 100, 0, 0), ("float32", 5, 3, 1), ("float16", 2048, 8, 0), ("bfloat16", 64, 3, 1), ("int8", 160, 5, 7), ("float32", 40, 3, 1),
                                               ("int64", 3, 0, 0)])
 @pytest.mark.parametrize("T,k", [(1, 8), (40, 1), (300, 3)])
 def test_moe_dispatch(env, dtype, K, pad, lead, T, k):
@@ -404,7 +404,7 @@ def combined(rows, pos, w, base):
 
 
 @pytest.mark.parametrize("rt,ot", [(a, b) for a in TYPES for b in TYPES])
-@pytest.mark.parametrize("T,k,M,pad,lead", [(1, 8, 64, 0, 0), (3, 1, 1, 0, 0), (37, 2, 333, 0, 0), (64, 3, 256, 8, 0), (20, 9, 130, 3, 1)])
+@pytest.mark.parametrize("T,k,M,pad,lead", [(1, 8, 64, 0, 0), (3, 1, 1, 0, 0), (37, 2, 333, 0, 0), (64, 3, 256, 8, 0), (20, 9, 130, 3, 1), (33, 2, 256, 3, 0)])
 @pytest.mark.parametrize("weighted,based", [(True, True), (False, False)])
 def test_moe_combine(env, rt, ot, T, k, M, pad, lead, weighted, based):
     torch, fp, ctx = env
@@ -455,7 +455,7 @@ def test_moe_combine_tokens_without_rows(env):
 
 @pytest.mark.parametrize("rt,ot", [("float32", "float32"), ("bfloat16", "bfloat16"), ("float16", "float32"), ("float32", "bfloat16"),
                                    ("bfloat16", "float16")])
-@pytest.mark.parametrize("T,k,M,pad,lead", [(1, 8, 64, 0, 0), (2, 1, 1, 0, 0), (37, 2, 333, 0, 0), (50, 5, 2048, 8, 0), (9, 3, 130, 3, 1)])
+@pytest.mark.parametrize("T,k,M,pad,lead", [(1, 8, 64, 0, 0), (2, 1, 1, 0, 0), (37, 2, 333, 0, 0), (50, 5, 2048, 8, 0), (9, 3, 130, 3, 1), (33, 4, 256, 3, 0), (1, 7, 1000, 3, 0)])
 def test_moe_combine_grad(env, rt, ot, T, k, M, pad, lead):
     torch, fp, ctx = env
     rng = np.random.default_rng(T + M)
@@ -488,6 +488,37 @@ def test_moe_combine_grad(env, rt, ot, T, k, M, pad, lead):
     ctx.moe_combine_grad(dout, rows, p, w, dweights=dw2)
     ctx.moe_combine_grad(dout, rows, p, w, drows=d2)
     assert torch.equal(dw2, dw) and torch.equal(d2, drows)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("pad,lead", [(3, 0), (1, 1), (5, 2), (7, 3)])
+def test_odd_inputs_dense_outputs(env, dtype, pad, lead):
+    # every input in rows of odd pitches, the outputs dense: loads from any address, to the matrices' ends
+    torch, fp, ctx = env
+    dt = getattr(torch, dtype)
+    rng = np.random.default_rng(pad)
+    T, k, M = 21, 2, 304
+
+    def odd(n):
+        t, _ = wide(torch, n, M, pad, dt, lead)
+        return t.copy_(torch.from_numpy(rng.standard_normal((n, M))).cuda())
+
+    x, rows, dout, base = odd(T), odd(T * k), odd(T), odd(T)
+    pos = torch.from_numpy(routed(rng, T, k, 4)).cuda()
+    w = torch.from_numpy(rng.random((T, k)).astype(np.float32)).cuda()
+
+    def run(x, rows, dout, base):
+        q, s = torch.zeros(T * k, M, dtype=torch.int8, device="cuda"), torch.zeros(T * k, device="cuda")
+        ctx.quantize_rows(x, q, s, pos=pos)
+        d, out = torch.zeros(T * k, M, dtype=dt, device="cuda"), torch.zeros(T, M, dtype=dt, device="cuda")
+        ctx.moe_dispatch(x, pos, d)
+        ctx.moe_combine(rows, pos, out, weights=w, base=base)
+        dr, dw = torch.zeros(T * k, M, dtype=dt, device="cuda"), torch.zeros(T, k, device="cuda")
+        ctx.moe_combine_grad(dout, rows, pos, w, dr, dw)
+        return q, s, d, out, dr, dw
+
+    for got, want in zip(run(x, rows, dout, base), run(*(t.contiguous() for t in (x, rows, dout, base)))):
+        assert torch.equal(got, want)
 
 
 def test_gradients_against_differences(env):
@@ -695,6 +726,45 @@ def test_capture_as_a_first_call(env):
         ctx.set_profiling(0)
     finally:
         ctx.close()
+
+
+def test_odd_pitches_in_graphs(env):
+    # products whose operands are realigned in the stream's memory: plain, captured twice, replayed side by side
+    torch, fp, ctx = env
+    runs = []
+    for i in range(2):
+        w, x, ws, xs, y, yb = product_case(torch, 90 + i, 150, 333, 0, "float32", 40 + i, padx=3)
+        st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            ctx.matmul_i8(w, x, y, ws, xs)
+        runs.append((w, x, ws, xs, y, st, g))
+    for _ in range(3):
+        for w, x, ws, xs, y, st, g in runs:
+            y.zero_()
+            x.copy_(torch.randint(-128, 128, x.shape, device="cuda"))
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for w, x, ws, xs, y, st, g in runs:
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for w, x, ws, xs, y, st, g in runs:
+            check_product(torch, w, x, ws, xs, y)
+            want = y.clone()
+            ctx.matmul_i8(w, x, y, ws, xs)
+            assert torch.equal(y, want)
+
+
+def test_odd_pitches_by_expert(env):
+    # experts without rows are not realigned; falling offsets do not hide one that has rows
+    torch, fp, ctx = env
+    for off, ends in (([0, 0, 5, 5, 9, 9], [0, 0, 5, 5, 9, 9]), ([0, 6, 2, 8, 8, 12], [0, 6, 6, 8, 8, 12])):
+        w, x, ws, xs, y, yb = product_case(torch, 12, 50, 77, 5, "float32", 50)
+        y.fill_(7)
+        ctx.matmul_i8(w, x, y, ws, xs, offsets=torch.tensor(off, dtype=torch.int32, device="cuda"))
+        check_product(torch, w, x, ws, xs, y, ends)
+        assert bool((y[ends[-1]:] == 7).all())
 
 
 def test_other_stream_explicitly(env):
