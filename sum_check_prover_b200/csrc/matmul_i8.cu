@@ -37,7 +37,7 @@ constexpr int MI_BM = 128;                  // channels per tile
 constexpr int MI_BK = 128;                  // bytes of K per k-tile
 constexpr int MI_W_BYTES = MI_BM * MI_BK;   // the weight box
 constexpr int MI_MAX_STAGES = 12;
-constexpr int MI_SMEM = 220 * 1024;         // dynamic shared memory of a block that has its SM alone
+constexpr int MI_SMEM = 200 * 1024;         // dynamic shared memory of a block that has its SM alone
 constexpr int MI_EPI_WARPS = 8;
 constexpr int MI_THREADS = 32 * (2 + MI_EPI_WARPS);
 constexpr uint32_t MI_WAIT_LIMIT = 1u << 24;
@@ -53,6 +53,7 @@ struct alignas(64) MiArgs {
     int64_t ldy;
     int32_t M, K, N, E;
     int32_t y_type;
+    int32_t yvec;            // rows of y hold whole aligned 16 bytes
     int32_t mt;              // channel tiles of an expert
     int32_t nk;              // k-tiles
     int32_t stages;
@@ -212,18 +213,40 @@ __device__ __forceinline__ int mi_columns(int cols) {
     return PAIR ? (cols + 31) & ~31 : (cols + 15) & ~15;
 }
 
-// y of 16 columns (tokens n .. n + cols - 1) for one channel
-template <typename YT>
-__device__ __forceinline__ void mi_store16(const MiArgs& a, const int32_t (&v)[16], int64_t n, int cols, int64_t m,
-                                           float ws, bool live, int lane) {
-    const float xl = (lane & 15) < cols ? __ldg(a.x_scale + n + (lane & 15)) : 0.0f;
-    YT* p = reinterpret_cast<YT*>(a.y) + n * a.ldy + m;
+// y of C columns (tokens n .. n + cols - 1) for 32 channels from m0 on, one a lane; xs: the tokens' scales.
+// The values cross the warp's C x 32 buffer in shared memory, so that a lane stores 16 bytes of a token
+// (a 2-byte store a lane and token took 24 instructions a token, most of them addresses and predicates).
+template <typename YT, int C>
+__device__ __forceinline__ void mi_store(const MiArgs& a, const int32_t (&v)[C], const float* xs, int64_t n, int cols,
+                                         int64_t m0, float ws, YT* buf, int lane) {
+    __syncwarp();  // the buffer's last values have been read
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-        const float xs = __shfl_sync(0xffffffffu, xl, i);
-        if (live && i < cols) *p = fp_from_f<YT>((float)v[i] * xs * ws);
-        p += a.ldy;
+    for (int i = 0; i < C; i++) buf[32 * i + lane] = fp_from_f<YT>((float)v[i] * xs[i] * ws);
+    __syncwarp();
+    constexpr int E16 = 16 / sizeof(YT), P = 32 / E16;  // values and pieces of 16 bytes
+    YT* y = reinterpret_cast<YT*>(a.y) + n * a.ldy + m0;
+    if (a.yvec) {
+        const int pc = lane % P;
+#pragma unroll
+        for (int i = 0; i < C * P / 32; i++) {
+            const int col = lane / P + i * (32 / P);
+            if (col < cols && m0 + pc * E16 < a.M)
+                *reinterpret_cast<uint4*>(y + col * a.ldy + pc * E16) = *reinterpret_cast<const uint4*>(buf + 32 * col + pc * E16);
+        }
+    } else if (m0 + lane < a.M) {
+#pragma unroll 4
+        for (int i = 0; i < cols; i++) y[i * a.ldy + lane] = buf[32 * i + lane];
     }
+}
+template <int C>
+__device__ __forceinline__ void mi_put(const MiArgs& a, const int32_t (&v)[C], const float* xs, int64_t n, int cols,
+                                       int64_t m0, float ws, void* buf, int lane) {
+    if (a.y_type == FP_F32)
+        mi_store<float>(a, v, xs, n, cols, m0, ws, (float*)buf, lane);
+    else if (a.y_type == FP_F16)
+        mi_store<__half>(a, v, xs, n, cols, m0, ws, (__half*)buf, lane);
+    else
+        mi_store<__nv_bfloat16>(a, v, xs, n, cols, m0, ws, (__nv_bfloat16*)buf, lane);
 }
 
 template <int BN, bool SPLIT, bool PAIR>
@@ -243,6 +266,9 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
     __shared__ uint32_t tmem_base;
     __shared__ volatile int s_abort;
     __shared__ int32_t s_part[32];
+    __shared__ __align__(16) float s_scale[MI_EPI_WARPS][128];
+    __shared__ __align__(16) uint8_t s_out[MI_EPI_WARPS][16 * 32 * 4];
+    static_assert(!SPLIT || BN <= 128, "a warp keeps the scales of 128 tokens");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nthr = blockDim.x;
     const int S = a.stages;
     uint32_t crank = 0, csize = 1;
@@ -446,20 +472,21 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
         for (int u = u0, m = mm0; u < total_u; tc++) {
             const MiTokens tk = mi_tokens(first, tiles, a.E, u);
             const uint32_t slot = tc % SLOTS;
-            const int64_t row = (int64_t)m * TM + wlead + 32 * qd + lane;
-            const bool live = row < a.M;
-            const float ws = live ? __ldg(a.w_scale + (int64_t)tk.e * a.M + row) : 0.0f;
+            const int64_t m0 = (int64_t)m * TM + wlead + 32 * qd;  // the warp's first channel
+            const float ws = m0 + lane < a.M ? __ldg(a.w_scale + (int64_t)tk.e * a.M + m0 + lane) : 0.0f;
+            // the scales of this warp's tokens, before their sums are there: chunk i of 16 columns at 16 i (SPLIT:
+            // all columns, for the share may lie anywhere)
+            float* xs = s_scale[warp - 2];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int j = lane + 32 * i, col = SPLIT ? j : (j >> 4) * 32 + 16 * part + (j & 15);
+                if (col < tk.cols) xs[j] = __ldg(a.x_scale + tk.n0 + col);
+            }
+            __syncwarp();
             if (!mi_wait_warp(mi_smem(&accfull[slot]), (tc / SLOTS) & 1u, &s_abort, err)) break;
             asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
             const uint32_t base = tmem + ((uint32_t)(32 * qd) << 16) + slot * BN;
-            auto put = [&](const int32_t(&v)[16], int c0, int cols) {
-                if (a.y_type == FP_F32)
-                    mi_store16<float>(a, v, (int64_t)tk.n0 + c0, cols, row, ws, live, lane);
-                else if (a.y_type == FP_F16)
-                    mi_store16<__half>(a, v, (int64_t)tk.n0 + c0, cols, row, ws, live, lane);
-                else
-                    mi_store16<__nv_bfloat16>(a, v, (int64_t)tk.n0 + c0, cols, row, ws, live, lane);
-            };
             if (!SPLIT) {
                 int32_t v[16], nx[16];
                 int c0 = 16 * part;
@@ -470,7 +497,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
 #pragma unroll 1
                 for (; c0 < tk.cols; c0 += 32) {
                     if (c0 + 32 < tk.cols) mi_ld16(base + (uint32_t)(c0 + 32), nx);
-                    put(v, c0, min(16, tk.cols - c0));
+                    mi_put<16>(a, v, xs + (c0 >> 5) * 16, (int64_t)tk.n0 + c0, min(16, tk.cols - c0), m0, ws, s_out[warp - 2], lane);
                     mi_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; i++) v[i] = nx[i];
@@ -507,14 +534,9 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
                 if (!got) break;
                 const int lo = (int)crank * per, hi = min(tk.cols, lo + per);
                 for (int c0 = lo + 8 * part; c0 < hi; c0 += 16) {
-                    int32_t v[16];
-                    {
-                        int32_t own[8];
-                        mi_ld8(base + (uint32_t)c0, own);
-                        mi_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 8; i++) v[i] = own[i], v[8 + i] = 0;
-                    }
+                    int32_t v[8];
+                    mi_ld8(base + (uint32_t)c0, v);
+                    mi_ld_wait();
                     const int cols = min(8, hi - c0);
                     for (uint32_t b = 0; b < csize; b++) {
                         if (b == crank) continue;
@@ -523,7 +545,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
                         for (int i = 0; i < 8; i++)
                             if (i < cols) v[i] += src[i * MI_BM];
                     }
-                    put(v, c0, cols);
+                    mi_put<8>(a, v, xs + c0, (int64_t)tk.n0 + c0, cols, m0, ws, s_out[warp - 2], lane);
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
@@ -659,6 +681,7 @@ int launch_mi(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x, int6
     a.per = SPLIT ? (((BN + split - 1) / split) + 7) & ~7 : 0;
     const size_t extra = (SPLIT ? (size_t)split * a.per * MI_BM * 4 : 0) + 8 * ((size_t)a.E + 1) + 1024;
     a.stages = (int)std::min<size_t>(MI_MAX_STAGES, (MI_SMEM - extra) / STAGE);
+    if (extra + 2 * STAGE > (size_t)MI_SMEM) return fp_fail(c, FP_ERR_SHAPE, "fp_matmul_i8: too many experts");  // (never: 3 stages at E = 4096)
     auto kern = matmul_i8_kernel<BN, SPLIT, PAIR>;
     FP_CUDA(c, fp_op_smem(c, 1 + (BN == 32 ? 0 : BN == 128 ? 4 : 8) + 2 * SPLIT + PAIR, kern, MI_SMEM));
     const int64_t tiles = token_tiles * a.mt;
@@ -734,6 +757,7 @@ int fp_matmul_i8(fp_ctx* c, const int8_t* w, int64_t ldw, const float* w_scale, 
     MiArgs a = {};
     a.w_scale = w_scale, a.x_scale = x_scale, a.offsets = offsets, a.y = y, a.ldy = ldy;
     a.M = (int32_t)M, a.K = (int32_t)K, a.N = (int32_t)N, a.E = E, a.y_type = y_type;
+    a.yvec = (M * ys) % 16 == 0 && fp_common_align({(uint64_t)(uintptr_t)y, (uint64_t)ldy * ys}) == 16;
     a.err = &c->mb_dev->op_err;
     // rows of a group: N of a dense product, twice the mean of those that can have rows by expert
     const int64_t rows = E == 1 ? N : 2 * ((N + std::min<int64_t>(E, N) - 1) / std::min<int64_t>(E, N));

@@ -474,9 +474,11 @@ int fp_moe_combine(fp_ctx* c, const void* rows, int rows_type, int64_t R, int64_
         by_type(out_type, [&](auto* op) {
             using OT = std::remove_pointer_t<decltype(op)>;
             constexpr int V = 16 / sizeof(RT), OA = V * sizeof(OT) < 16 ? V * sizeof(OT) : 16;
-            const bool vec = M % V == 0 && fp_common_align({(uint64_t)(uintptr_t)out, (uint64_t)ldo * os}) >= OA;
             const bool aligned = fp_common_align({(uint64_t)(uintptr_t)rows, (uint64_t)ldr * rs}) == 16 &&
                                  fp_common_align({(uint64_t)(uintptr_t)base, (uint64_t)ldb * os}) >= OA;
+            // fp32 rows at odd addresses: single values (7281 x 712, k = 4: 25.6 us, and 33.9 shifted)
+            const bool vec = M % V == 0 && fp_common_align({(uint64_t)(uintptr_t)out, (uint64_t)ldo * os}) >= OA &&
+                             (aligned || rs == 2);
             const int nvec = (int)(vec ? M / V : M);
             auto run = [&](auto kern, int loads) {
                 const FpRowGrid g = fp_row_grid(c, T, nvec, loads, true);
