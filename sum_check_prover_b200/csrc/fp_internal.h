@@ -138,6 +138,7 @@ struct fp_ctx {
     int tc_gemm = 2;
     FpMmPoint mm_point;
     cudaMemPool_t pool = nullptr;  // stream-ordered scratch of operators (rows that TMA cannot read)
+    int16_t op_clusters[2][8] = {};  // by kernel and cluster size, 1 + the clusters that fit on the GPU; 0: not asked yet
     uint32_t op_smem = 0;  // operator kernels whose shared-memory limit has been raised on this device, a bit each
     // timing
     int profiling = 0;

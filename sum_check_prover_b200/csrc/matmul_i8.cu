@@ -307,6 +307,14 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
         }
     }
+    // what is above overlaps the end of the kernel before this one on the stream; from here on its results are
+    // read. The next kernel may be brought onto the SMs that this one leaves.
+    if (warp == 0 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(&a.tw) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(&a.tx) : "memory");
+    }
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     // the experts' first rows (each offset counted as the largest up to it, inside [0, N]) and the prefix
     // sums of their token tiles
     if (!a.offsets) {
@@ -670,6 +678,11 @@ int mi_realign(fp_ctx* c, MiOperand& o, int K, const int32_t* offsets, int M, in
 }
 
 template <int BN, bool SPLIT, bool PAIR>
+constexpr int mi_kernel_bit() {
+    return 1 + (BN == 32 ? 0 : BN == 128 ? 4 : 8) + 2 * SPLIT + PAIR;
+}
+
+template <int BN, bool SPLIT, bool PAIR>
 int launch_mi(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x, int64_t token_tiles, int split, cudaStream_t st) {
     constexpr int STAGE = MI_W_BYTES + (PAIR ? BN / 2 : BN) * MI_BK;
     constexpr int TM = PAIR ? 2 * MI_BM : MI_BM;
@@ -683,21 +696,50 @@ int launch_mi(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x, int6
     a.stages = (int)std::min<size_t>(MI_MAX_STAGES, (MI_SMEM - extra) / STAGE);
     if (extra + 2 * STAGE > (size_t)MI_SMEM) return fp_fail(c, FP_ERR_SHAPE, "fp_matmul_i8: too many experts");  // (never: 3 stages at E = 4096)
     auto kern = matmul_i8_kernel<BN, SPLIT, PAIR>;
-    FP_CUDA(c, fp_op_smem(c, 1 + (BN == 32 ? 0 : BN == 128 ? 4 : 8) + 2 * SPLIT + PAIR, kern, MI_SMEM));
+    FP_CUDA(c, fp_op_smem(c, mi_kernel_bit<BN, SPLIT, PAIR>(), kern, MI_SMEM));
     const int64_t tiles = token_tiles * a.mt;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(cluster * (SPLIT ? tiles : std::min<int64_t>(tiles, c->num_sms / cluster))));
     cfg.blockDim = dim3(MI_THREADS);
     cfg.dynamicSmemBytes = a.stages * STAGE + extra;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     FP_CUDA(c, cudaLaunchKernelEx(&cfg, kern, a));
     return FP_OK;
+}
+
+// clusters of `split` blocks of the splitting kernel that the GPU holds at once (asked once a context)
+template <int BN>
+int64_t mi_clusters(fp_ctx* c, int split) {
+    int16_t& n = c->op_clusters[BN == 32 ? 0 : 1][split];
+    if (n == 0) {
+        auto kern = matmul_i8_kernel<BN, true, false>;
+        if (fp_op_smem(c, mi_kernel_bit<BN, true, false>(), kern, MI_SMEM) != cudaSuccess) return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)split);
+        cfg.blockDim = dim3(MI_THREADS);
+        cfg.dynamicSmemBytes = MI_SMEM;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)split;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int most = 0;
+        if (cudaOccupancyMaxActiveClusters(&most, kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            most = 0;
+        }
+        n = (int16_t)(most + 1);
+    }
+    return n - 1;
 }
 
 // token tiles at most: every group that can have rows has one, and the rows fill the others
@@ -706,17 +748,33 @@ int64_t mi_token_tiles(const MiArgs& a, int bn) {
     return groups == 1 ? (a.N + bn - 1) / bn : groups + a.N / bn;
 }
 
+// The sums over K are split when the tiles of a whole K leave SMs idle: as far as all clusters are on the GPU at
+// once (a second wave costs what the split gains: 64 tiles of 8192 x 5120, 16 tokens, took 13.8 us in two parts
+// and 20.9 in three), up to six parts of at least four k-tiles (1 x 5120 x 16384, 40 tiles: 37.5, 23.5 and 20.1
+// us whole and in two and three parts; 1 x 1024 x 8192, 8 tiles: 20.7 us whole, 14.1, 10.4 and 9.8 in two, four
+// and six).
+template <int BN>
+int mi_split(fp_ctx* c, int64_t tiles, int64_t nk) {
+    for (int s = (int)std::min<int64_t>(6, nk / 4); s > 1; s--)
+        if (tiles <= c->num_sms / s && tiles <= mi_clusters<BN>(c, s)) return s;
+    return 1;
+}
+
+// Tiles of 32 tokens where a group has no more (deeper stages), else of 128 where K can be split, else pairs
 int launch_product(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x, int64_t rows, cudaStream_t st) {
     const int64_t mt = (a.M + MI_BM - 1) / MI_BM, nk = (a.K + MI_BK - 1) / MI_BK;
     a.nk = (int32_t)nk;
-    const int bn = rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
-    const int64_t tt = mi_token_tiles(a, bn);
-    int split = 1;
-    while (bn <= 128 && split < 8 && tt * mt * split * 2 <= c->num_sms && split * 4 <= nk) split *= 2;
-    if (bn == 32)
+    if (rows <= 32) {
+        const int64_t tt = mi_token_tiles(a, 32);
+        const int split = mi_split<32>(c, tt * mt, nk);
         return split > 1 ? launch_mi<32, true, false>(c, a, w, x, tt, split, st)
                          : launch_mi<32, false, false>(c, a, w, x, tt, 1, st);
-    if (split > 1) return launch_mi<128, true, false>(c, a, w, x, tt, split, st);
+    }
+    if (rows <= 128) {
+        const int64_t tt = mi_token_tiles(a, 128);
+        const int split = mi_split<128>(c, tt * mt, nk);
+        if (split > 1) return launch_mi<128, true, false>(c, a, w, x, tt, split, st);
+    }
     return launch_mi<256, false, true>(c, a, w, x, mi_token_tiles(a, 256), 1, st);
 }
 
