@@ -750,17 +750,20 @@ int64_t mi_token_tiles(const MiArgs& a, int bn) {
 
 // The sums over K are split when the tiles of a whole K leave SMs idle: as far as all clusters are on the GPU at
 // once (a second wave costs what the split gains: 64 tiles of 8192 x 5120, 16 tokens, took 13.8 us in two parts
-// and 20.9 in three), up to six parts of at least four k-tiles (1 x 5120 x 16384, 40 tiles: 37.5, 23.5 and 20.1
+// and 20.9 in three), from twelve k-tiles up to six parts of at least four (700 x 1024 x 1024, eight: 7.3 us whole, 8.6 in two;
+// 1 x 5120 x 16384, 40 tiles: 37.5, 23.5 and 20.1
 // us whole and in two and three parts; 1 x 1024 x 8192, 8 tiles: 20.7 us whole, 14.1, 10.4 and 9.8 in two, four
 // and six).
 template <int BN>
 int mi_split(fp_ctx* c, int64_t tiles, int64_t nk) {
-    for (int s = (int)std::min<int64_t>(6, nk / 4); s > 1; s--)
+    for (int s = nk < 12 ? 1 : (int)std::min<int64_t>(6, nk / 4); s > 1; s--)
         if (tiles <= c->num_sms / s && tiles <= mi_clusters<BN>(c, s)) return s;
     return 1;
 }
 
-// Tiles of 32 tokens where a group has no more (deeper stages), else of 128 where K can be split, else pairs
+// Tiles of 32 tokens where a group has no more (deeper stages); of 128 where all such tiles are on the GPU at
+// once, K split or whole (512 x 4096 x 4096: 16.2 us, pairs 17.7; 256 x 2048 x 8192: 14.2 and 26.1); else pairs
+// (1024 x 4096 x 4096: 18.2 us, tiles of 128 25.1)
 int launch_product(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x, int64_t rows, cudaStream_t st) {
     const int64_t mt = (a.M + MI_BM - 1) / MI_BM, nk = (a.K + MI_BK - 1) / MI_BK;
     a.nk = (int32_t)nk;
@@ -770,10 +773,11 @@ int launch_product(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x,
         return split > 1 ? launch_mi<32, true, false>(c, a, w, x, tt, split, st)
                          : launch_mi<32, false, false>(c, a, w, x, tt, 1, st);
     }
-    if (rows <= 128) {
-        const int64_t tt = mi_token_tiles(a, 128);
+    const int64_t tt = mi_token_tiles(a, 128);
+    if (tt * mt <= c->num_sms) {
         const int split = mi_split<128>(c, tt * mt, nk);
-        if (split > 1) return launch_mi<128, true, false>(c, a, w, x, tt, split, st);
+        return split > 1 ? launch_mi<128, true, false>(c, a, w, x, tt, split, st)
+                         : launch_mi<128, false, false>(c, a, w, x, tt, 1, st);
     }
     return launch_mi<256, false, true>(c, a, w, x, mi_token_tiles(a, 256), 1, st);
 }
