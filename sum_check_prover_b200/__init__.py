@@ -624,14 +624,14 @@ def _stream(stream) -> Optional[int]:
 
 
 _REAL = {"float32": 0, "float16": 1, "bfloat16": 2}  # FP_F32, FP_F16, FP_BF16
-_DTYPES: dict = {}  # a tensor's dtype -> (its name, its FP_ type or None): a lookup per tensor and call
+_DTYPES: dict = {}  # a tensor's dtype -> its name: a lookup per tensor and call
 
 
-def _dtype(dt) -> tuple:
+def _dtype(t) -> str:
+    dt = t.dtype
     got = _DTYPES.get(dt)
     if got is None:
-        name = str(dt).rsplit(".", 1)[-1]
-        got = _DTYPES[dt] = (name, _REAL.get(name))
+        got = _DTYPES[dt] = str(dt).rsplit(".", 1)[-1]
     return got
 
 
@@ -1020,49 +1020,48 @@ class Context:
                 lambda device: torch.cuda.current_stream(device).cuda_stream)
         return _raw_stream(self.device)
 
-    def _at(self, what: str, name: str, t) -> int:
-        """The address of a tensor on the context's device."""
+    def _refuse(self, what: str, name: str, t, shape, dtype: Optional[str], dense: bool):
+        """Say what is wrong with a tensor (shape: None for any extent)."""
+        if len(t.shape) != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape)):
+            raise ValueError(f"{what}: {name} must be {_times('?' if x is None else x for x in shape)}, not {_times(t.shape)}")
+        if dtype is not None and _dtype(t) != dtype:
+            raise ValueError(f"{what}: {name} must be {dtype}, not {_dtype(t)}")
         if t.get_device() != self.device:
             raise ValueError(f"{what}: {name} must be on cuda:{self.device}, not {t.device}")
-        return t.data_ptr()
+        raise ValueError(f"{what}: {name} must be contiguous" if dense else
+                         f"{what}: {name}'s rows must be contiguous and apart")
 
     def _dense(self, what: str, name: str, t, shape: tuple, dtype: str) -> int:
-        """Check a contiguous tensor of one shape and type; its address."""
-        if t.shape != shape:
-            raise ValueError(f"{what}: {name} must be {_times(shape)}, not {_times(t.shape)}")
-        if _dtype(t.dtype)[0] != dtype:
-            raise ValueError(f"{what}: {name} must be {dtype}, not {_dtype(t.dtype)[0]}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: {name} must be contiguous")
-        return self._at(what, name, t)
+        """Check a contiguous tensor of one shape and type on the context's device; its address."""
+        if t.shape != shape or _dtype(t) != dtype or t.get_device() != self.device or not t.is_contiguous():
+            self._refuse(what, name, t, shape, dtype, True)
+        return t.data_ptr()
 
-    def _rows(self, what: str, name: str, t, rows: Optional[int] = None, cols: Optional[int] = None,
-              dtype: Optional[str] = None) -> tuple:
-        """Check a two-dimensional tensor whose rows may be part of wider ones; (address, rows, columns,
-        row pitch)."""
+    def _rows(self, what: str, name: str, t, rows: Optional[int], cols: Optional[int], dtype: Optional[str]) -> tuple:
+        """Check a two-dimensional tensor on the context's device whose rows may be part of wider ones;
+        (address, rows, columns, row pitch)."""
         shape = t.shape
-        if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
-            want = _times("?" if x is None else x for x in (rows, cols))
-            raise ValueError(f"{what}: {name} must be {want}, not {_times(shape)}")
-        if dtype is not None and _dtype(t.dtype)[0] != dtype:
-            raise ValueError(f"{what}: {name} must be {dtype}, not {_dtype(t.dtype)[0]}")
+        if len(shape) != 2:
+            self._refuse(what, name, t, (rows, cols), dtype, False)
         n, m = shape
         ld, step = t.stride()
-        if (m > 1 and step != 1) or (n > 1 and ld < m):
-            raise ValueError(f"{what}: {name}'s rows must be contiguous and apart")
-        return self._at(what, name, t), n, m, (ld if n > 1 else m)
+        if ((rows is not None and n != rows) or (cols is not None and m != cols) or t.get_device() != self.device
+                or (dtype is not None and _dtype(t) != dtype) or (step != 1 and m > 1) or (ld < m and n > 1)):
+            self._refuse(what, name, t, (rows, cols), dtype, False)
+        return t.data_ptr(), n, m, (ld if n > 1 else m)
 
     def _real(self, what: str, name: str, t) -> int:
-        dt, code = _dtype(t.dtype)
+        code = _REAL.get(_dtype(t))
         if code is None:
-            raise ValueError(f"{what}: {name} must be float32, float16 or bfloat16, not {dt}")
+            raise ValueError(f"{what}: {name} must be float32, float16 or bfloat16, not {_dtype(t)}")
         return code
 
     def _positions(self, what: str, pos, T: int) -> tuple:
         """(address, choices a token) of T x k int32 positions."""
-        if len(pos.shape) != 2:
-            raise ValueError(f"{what}: pos must be {T} x ?, not {_times(pos.shape)}")
-        k = pos.shape[1]
+        shape = pos.shape
+        if len(shape) != 2:
+            self._refuse(what, "pos", pos, (T, None), "int32", True)
+        k = shape[1]
         return self._dense(what, "pos", pos, (T, k), "int32"), k
 
     def quantize_rows(self, x, q, scale, pos=None, stream=None) -> None:
@@ -1070,7 +1069,7 @@ class Context:
         x: T x K float32, float16 or bfloat16; q: R x K int8; scale: R float32. pos (T x k int32, from
         moe_sort): token t goes to the rows pos[t], else to row t. Rows without a token are left."""
         what = "quantize_rows"
-        xp, T, K, ldx = self._rows(what, "x", x)
+        xp, T, K, ldx = self._rows(what, "x", x, None, None, None)
         xt = self._real(what, "x", x)
         qp, R, _, ldq = self._rows(what, "q", q, None, K, "int8")
         sp = self._dense(what, "scale", scale, (R,), "float32")
@@ -1100,7 +1099,7 @@ class Context:
             op = self._dense(what, "offsets", offsets, (E + 1,), "int32")
         xp, N, _, ldx = self._rows(what, "x", x, None, K, "int8")
         xsp = self._dense(what, "x_scale", x_scale, (N,), "float32")
-        yp, _, _, ldy = self._rows(what, "y", y, N, M)
+        yp, _, _, ldy = self._rows(what, "y", y, N, M, None)
         rc = self._L.fp_matmul_i8(self.h, wp, ldw, wsp, E, M, K, xp, ldx, xsp, N, op, yp, self._real(what, "y", y), ldy,
                                   self._op_stream(stream))
         if rc:
@@ -1124,8 +1123,8 @@ class Context:
         experts' inputs of prove_dispatch, for any k. Rows without a token are left. Its gradient is
         moe_combine without weights."""
         what = "moe_dispatch"
-        xp, T, K, ldx = self._rows(what, "x", x)
-        rp, R, _, ldr = self._rows(what, "rows", rows, None, K, _dtype(x.dtype)[0])
+        xp, T, K, ldx = self._rows(what, "x", x, None, None, None)
+        rp, R, _, ldr = self._rows(what, "rows", rows, None, K, _dtype(x))
         pp, k = self._positions(what, pos, T)
         size = x.element_size()
         rc = self._L.fp_moe_dispatch(self.h, xp, T, K * size, ldx * size, pp, k, R, rp, ldr * size,
@@ -1138,11 +1137,11 @@ class Context:
         float32, float16 or bfloat16; pos: T x k int32; weights: T x k float32 or None (ones); base: as out
         (it may be out) or None."""
         what = "moe_combine"
-        rp, R, M, ldr = self._rows(what, "rows", rows)
-        op, T, _, ldo = self._rows(what, "out", out, None, M)
+        rp, R, M, ldr = self._rows(what, "rows", rows, None, None, None)
+        op, T, _, ldo = self._rows(what, "out", out, None, M, None)
         pp, k = self._positions(what, pos, T)
         wp = self._dense(what, "weights", weights, (T, k), "float32") if weights is not None else None
-        bp, _, _, ldb = self._rows(what, "base", base, T, M, _dtype(out.dtype)[0]) if base is not None else (None, 0, 0, 0)
+        bp, _, _, ldb = self._rows(what, "base", base, T, M, _dtype(out)) if base is not None else (None, 0, 0, 0)
         rc = self._L.fp_moe_combine(self.h, rp, self._real(what, "rows", rows), R, ldr, pp, wp, bp, ldb, T, k, M, op,
                                     self._real(what, "out", out), ldo, self._op_stream(stream))
         if rc:
@@ -1153,12 +1152,12 @@ class Context:
         dweights[t][j] = <dout[t], rows[pos[t][j]]> (T x k float32), either of them None when it is not
         wanted. dout: T x M (base's gradient as it is). Rows of drows without a choice are left."""
         what = "moe_combine_grad"
-        dp, T, M, ldd = self._rows(what, "dout", dout)
-        rp, R, _, ldr = self._rows(what, "rows", rows, None, M)
+        dp, T, M, ldd = self._rows(what, "dout", dout, None, None, None)
+        rp, R, _, ldr = self._rows(what, "rows", rows, None, M, None)
         pp, k = self._positions(what, pos, T)
         wp = self._dense(what, "weights", weights, (T, k), "float32") if weights is not None else None
         dwp = self._dense(what, "dweights", dweights, (T, k), "float32") if dweights is not None else None
-        gp, _, _, ldg = self._rows(what, "drows", drows, R, M, _dtype(rows.dtype)[0]) if drows is not None else (None, 0, 0, 0)
+        gp, _, _, ldg = self._rows(what, "drows", drows, R, M, _dtype(rows)) if drows is not None else (None, 0, 0, 0)
         rc = self._L.fp_moe_combine_grad(self.h, dp, self._real(what, "dout", dout), ldd, rp,
                                          self._real(what, "rows", rows), R, ldr, pp, wp, T, k, M, gp, ldg, dwp,
                                          self._op_stream(stream))

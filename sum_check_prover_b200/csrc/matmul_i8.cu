@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
         }
     }
     // what is above overlaps the end of the kernel before this one on the stream; from here on its results are
-    // read. The next kernel may be brought onto the SMs that this one leaves.
+    // read (with plain loads: an invariant one could be moved up across the wait). The next kernel may be brought
+    // onto the SMs that this one leaves.
     if (warp == 0 && lane == 0) {
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(&a.tw) : "memory");
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(&a.tx) : "memory");
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
     } else {
         const int per = (a.E + nthr) / nthr, x0 = min(a.E + 1, tid * per), x1 = min(a.E + 1, x0 + per);
         int32_t m = 0;
-        for (int x = x0; x < x1; x++) m = max(m, __ldg(a.offsets + x));
+        for (int x = x0; x < x1; x++) m = max(m, a.offsets[x]);
         int32_t inc = m;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
         if (lane == 0) run = 0;
         for (int w = 0; w < warp; w++) run = max(run, s_part[w]);
         for (int x = x0; x < x1; x++) {
-            run = max(run, __ldg(a.offsets + x));
+            run = max(run, a.offsets[x]);
             first[x] = min(run, a.N);
         }
         __syncthreads();
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
             const MiTokens tk = mi_tokens(first, tiles, a.E, u);
             const uint32_t slot = tc % SLOTS;
             const int64_t m0 = (int64_t)m * TM + wlead + 32 * qd;  // the warp's first channel
-            const float ws = m0 + lane < a.M ? __ldg(a.w_scale + (int64_t)tk.e * a.M + m0 + lane) : 0.0f;
+            const float ws = m0 + lane < a.M ? a.w_scale[(int64_t)tk.e * a.M + m0 + lane] : 0.0f;
             // the scales of this warp's tokens, before their sums are there: chunk i of 16 columns at 16 i (SPLIT:
             // all columns, for the share may lie anywhere)
             float* xs = s_scale[warp - 2];
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const int j = lane + 32 * i, col = SPLIT ? j : (j >> 4) * 32 + 16 * part + (j & 15);
-                if (col < tk.cols) xs[j] = __ldg(a.x_scale + tk.n0 + col);
+                if (col < tk.cols) xs[j] = a.x_scale[tk.n0 + col];
             }
             __syncwarp();
             if (!mi_wait_warp(mi_smem(&accfull[slot]), (tc / SLOTS) & 1u, &s_abort, err)) break;
@@ -750,10 +751,9 @@ int64_t mi_token_tiles(const MiArgs& a, int bn) {
 
 // The sums over K are split when the tiles of a whole K leave SMs idle: as far as all clusters are on the GPU at
 // once (a second wave costs what the split gains: 64 tiles of 8192 x 5120, 16 tokens, took 13.8 us in two parts
-// and 20.9 in three), from twelve k-tiles up to six parts of at least four (700 x 1024 x 1024, eight: 7.3 us whole, 8.6 in two;
-// 1 x 5120 x 16384, 40 tiles: 37.5, 23.5 and 20.1
-// us whole and in two and three parts; 1 x 1024 x 8192, 8 tiles: 20.7 us whole, 14.1, 10.4 and 9.8 in two, four
-// and six).
+// and 20.9 in three), from twelve k-tiles on, up to six parts of at least four (700 x 1024 x 1024, eight k-tiles:
+// 7.3 us whole, 8.6 in two; 1 x 5120 x 16384, 40 tiles: 37.5, 23.5 and 20.1 us whole and in two and three parts;
+// 1 x 1024 x 8192, 8 tiles: 20.7 us whole, 14.1, 10.4 and 9.8 in two, four and six).
 template <int BN>
 int mi_split(fp_ctx* c, int64_t tiles, int64_t nk) {
     for (int s = nk < 12 ? 1 : (int)std::min<int64_t>(6, nk / 4); s > 1; s--)

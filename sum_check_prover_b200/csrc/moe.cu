@@ -541,7 +541,7 @@ int fp_moe_combine_grad(fp_ctx* c, const void* dout, int out_type, int64_t ldd, 
             auto run = [&](auto kern, int loads) {
                 FpRowGrid g = fp_row_grid(c, T, nvec, loads, false);
                 if (T * nvec < (int64_t)c->num_sms * 1024) {  // few tokens: wider blocks, the choices over blocks
-                    while (g.tpr < MO_GRAD_THREADS && g.tpr * loads < nvec) g.tpr *= 2;
+                    while (g.tpr < MO_GRAD_THREADS && g.tpr * loads < nvec) g.tpr = std::min(MO_GRAD_THREADS, 2 * g.tpr);
                     g.rpb = std::max(1, FP_ROW_THREADS / g.tpr);
                     g.gx = (unsigned)((T + g.rpb - 1) / g.rpb);
                     g.gy = (unsigned)std::min(k / 2 + (k & 1), 32);

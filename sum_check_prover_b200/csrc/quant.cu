@@ -41,17 +41,17 @@ __device__ __forceinline__ float quant_exact(float x, const QuantRow& row) {
     return copysignf(n, x);
 }
 
-// V values to int8
-template <typename T, int V>
+// V values to int8; ONE: each by quant_exact
+template <typename T, int V, bool ONE>
 __device__ __forceinline__ FpWords<V> quant_vec(const FpVec<T, V>& w, const QuantRow& row) {
     float n[V], off = 0.0f;
 #pragma unroll
-    for (int e = 0; e < V; e++) {
+    for (int e = 0; e < V && !ONE; e++) {
         const float t = w.get(e) * row.inv;
         n[e] = t + QR_MAGIC;
         if (sizeof(T) == 4) off = fmaxf(off, fabsf(t - (n[e] - QR_MAGIC)));
     }
-    if (off > QR_NEAR || row.exact) {
+    if (ONE || off > QR_NEAR) {
 #pragma unroll
         for (int e = 0; e < V; e++) n[e] = quant_exact(w.get(e), row) + QR_MAGIC;
     }
@@ -73,12 +73,13 @@ __device__ __forceinline__ FpWords<V> quant_vec(const FpVec<T, V>& w, const Quan
 // to a word
 template <typename T, int V>
 __device__ __forceinline__ uint32_t quant_largest(const FpVec<T, V>& w, uint32_t m) {
+    constexpr int W = FpVec<T, V>::W;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < FpVec<T, V>::W; i++) {
-        if constexpr (sizeof(T) == 4)
-            m = max(m, w.w[i] & 0x7fffffffu);
-        else
-            m = __vmaxu2(m, w.w[i] & 0x7fff7fffu);
+        for (int i = 0; i < W; i++) m = max(m, w.w[i] & 0x7fffffffu);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 2) m = __vimax3_u16x2(m, w.w[i] & 0x7fff7fffu, W > 1 ? w.w[i + (W > 1)] & 0x7fff7fffu : 0u);
     }
     return m;
 }
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(256, 4)
     const int copies = pos ? k : 1;
     FpWords<V> o[NV];
 #pragma unroll
-    for (int i = 0; i < NV; i++) o[i] = quant_vec<T, V>(reg[i], r);
+    for (int i = 0; i < NV; i++) o[i] = quant_vec<T, V, false>(reg[i], r);
     for (int j = 0; j < copies; j++) {
         const int64_t p = j == 0 ? p0 : __ldg(pos + row * k + j);
         if (p < 0 || p >= R) continue;
@@ -154,13 +155,22 @@ __global__ void __launch_bounds__(256, 4)
                 for (int e = 0; e < V; e++) d[c * V + e] = (int8_t)(w.w[e >> 2] >> (8 * (e & 3)));
             }
         };
+        if (r.exact) {  // (the same in all of a row's threads; the row is read again)
+#pragma unroll 1
+            for (int c = t; c < nvec; c += tpr) {
+                FpVec<T, V> w;
+                w.template load_row<ANY>(xr + c * V, span);
+                put(c, quant_vec<T, V, true>(w, r));
+            }
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < NV; i++)
             if (t + i * tpr < nvec) put(t + i * tpr, o[i]);
         for (int c = t + NV * tpr; c < nvec; c += tpr) {
             FpVec<T, V> w;
             w.template load_row<ANY>(xr + c * V, span);
-            put(c, quant_vec<T, V>(w, r));
+            put(c, quant_vec<T, V, false>(w, r));
         }
     }
 }
