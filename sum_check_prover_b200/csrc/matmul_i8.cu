@@ -121,8 +121,8 @@ __device__ __forceinline__ bool mi_wait_warp(uint32_t bar, uint32_t parity, vola
 // the same for copies and MMAs in flight while aborting: no flag is looked at
 __device__ __forceinline__ void mi_drain(uint32_t bar, uint32_t parity) { mi_wait_scope<false>(bar, parity, nullptr, nullptr); }
 
-__device__ __forceinline__ void mi_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mi_arrive(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
 }
 // arrives when the MMAs issued so far are complete; PAIR: at the barrier of that offset in both blocks
 template <bool PAIR>
@@ -135,11 +135,11 @@ __device__ __forceinline__ void mi_commit(uint32_t bar) {
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
-// an arrival at the barrier of that offset in block `rank` of the cluster
-__device__ __forceinline__ void mi_arrive_at(uint32_t bar, uint32_t rank) {
+// arrivals at the barrier of that offset in block `rank` of the cluster
+__device__ __forceinline__ void mi_arrive_at(uint32_t bar, uint32_t rank, uint32_t count) {
     uint32_t there;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(bar), "r"(rank));
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(there) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0], %1;\n" ::"r"(there), "r"(count) : "memory");
 }
 // a, b: the low words of the operands' descriptors
 template <bool PAIR>
@@ -475,12 +475,24 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
         __syncwarp();
     } else if (warp >= 2) {
         // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31; the two warps of the same lanes take every
-        // other chunk of 16 columns, the next one's load in flight while one is stored ----
-        const int qd = warp & 3, part = (warp - 2) >> 2;
+        // other chunk of 16 columns of a tile, or, of tiles with few columns, whose time is mostly the way to
+        // the scales and back, every other tile. A chunk's load is in flight while the one before is stored
+        // (53 experts, 1649 tokens, 2992 x 96: 20.7 us, tiles shared 23.5).
+        const int qd = warp & 3, group = (warp - 2) >> 2;
+        const bool several = (int64_t)total_u * a.mt > walkers;  // some block has more than one tile
         uint32_t tc = 0;
         for (int u = u0, m = mm0; u < total_u; tc++) {
             const MiTokens tk = mi_tokens(first, tiles, a.E, u);
             const uint32_t slot = tc % SLOTS;
+            const bool alone = !SPLIT && several && tk.cols <= 64;  // a group's own tile
+            if (alone && (int)(tc & 1) != group) {
+                // (the other's; the wait keeps this warp's count of the barrier's phases)
+                if (!mi_wait_warp(mi_smem(&accfull[slot]), (tc / SLOTS) & 1u, &s_abort, err)) break;
+                u += du, m += dm;
+                if (m >= a.mt) m -= a.mt, u++;
+                continue;
+            }
+            const int part = alone ? 0 : group, step = alone ? 16 : 32;
             const int64_t m0 = (int64_t)m * TM + wlead + 32 * qd;  // the warp's first channel
             const float ws = m0 + lane < a.M ? a.w_scale[(int64_t)tk.e * a.M + m0 + lane] : 0.0f;
             // the scales of this warp's tokens, before their sums are there: chunk i of 16 columns at 16 i (SPLIT:
@@ -489,7 +501,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const int j = lane + 32 * i, col = SPLIT ? j : (j >> 4) * 32 + 16 * part + (j & 15);
+                const int j = lane + 32 * i, col = SPLIT || alone ? j : (j >> 4) * 32 + 16 * part + (j & 15);
                 if (col < tk.cols) xs[j] = a.x_scale[tk.n0 + col];
             }
             __syncwarp();
@@ -504,9 +516,9 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
                     mi_ld_wait();
                 }
 #pragma unroll 1
-                for (; c0 < tk.cols; c0 += 32) {
-                    if (c0 + 32 < tk.cols) mi_ld16(base + (uint32_t)(c0 + 32), nx);
-                    mi_put<16>(a, v, xs + (c0 >> 5) * 16, (int64_t)tk.n0 + c0, min(16, tk.cols - c0), m0, ws, s_out[warp - 2], lane);
+                for (; c0 < tk.cols; c0 += step) {
+                    if (c0 + step < tk.cols) mi_ld16(base + (uint32_t)(c0 + step), nx);
+                    mi_put<16>(a, v, xs + (alone ? c0 : (c0 >> 5) * 16), (int64_t)tk.n0 + c0, min(16, tk.cols - c0), m0, ws, s_out[warp - 2], lane);
                     mi_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; i++) v[i] = nx[i];
@@ -515,7 +527,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
                 // send: columns [d per, (d + 1) per) to block d, at [this block][column][lane]; the two warps of
                 // the same lanes take every other block
                 const int per = a.per, mrow = 32 * qd + lane;
-                for (uint32_t d = (uint32_t)part; d < csize; d += 2) {
+                for (uint32_t d = (uint32_t)group; d < csize; d += 2) {
                     if (d == crank) continue;
                     const int lo = (int)d * per, hi = min(tk.cols, lo + per);
                     uint32_t at;
@@ -535,14 +547,14 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) {
                     for (uint32_t d = 0; d < csize; d++)
-                        if (d != crank) mi_arrive_at(mi_smem(&redfull), d);
+                        if (d != crank) mi_arrive_at(mi_smem(&redfull), d, 1);
                 }
                 __syncwarp();
                 const bool got =
                     csize == 1 || __all_sync(0xffffffffu, mi_wait_scope<true>(mi_smem(&redfull), 0, &s_abort, err));
                 if (!got) break;
                 const int lo = (int)crank * per, hi = min(tk.cols, lo + per);
-                for (int c0 = lo + 8 * part; c0 < hi; c0 += 16) {
+                for (int c0 = lo + 8 * group; c0 < hi; c0 += 16) {
                     int32_t v[8];
                     mi_ld8(base + (uint32_t)c0, v);
                     mi_ld_wait();
@@ -560,10 +572,11 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
             asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
             __syncwarp();
             if (lane == 0) {
+                // (the four warps of a tile of their own arrive for the other four)
                 if (PAIR)
-                    mi_arrive_at(mi_smem(&accempty[slot]), 0);
+                    mi_arrive_at(mi_smem(&accempty[slot]), 0, alone ? 2 : 1);
                 else
-                    mi_arrive(mi_smem(&accempty[slot]));
+                    mi_arrive(mi_smem(&accempty[slot]), alone ? 2 : 1);
             }
             u += du, m += dm;
             if (m >= a.mt) m -= a.mt, u++;
