@@ -23,6 +23,17 @@
 // blocks exchange their int32 partial sums through distributed shared memory: block d of the cluster
 // finishes the d-th share of the columns. Integer sums have no order, so the split changes no bit.
 //
+// What bounds it, and what it takes (B200, repeated calls on changing inputs):
+//   many tokens    the tensor cores: 4096 x 14336 x 4096 157-161 us, 3.0 PTOP/s, 0.9 of twice the measured bf16
+//                  rate, tensor pipe 85% active. One block a tile of 128 x 256 took 187 us: its operands came to
+//                  1.5 times the L2 traffic, 15 TB/s.
+//   few a group    HBM: 128 experts of 8192 x 5120, 8192 tokens, 833 us, 6.6 TB/s; 64 tokens 276 us, 6.9.
+//   one weight     the way in and out: 5120 x 16384 for one token takes 19 us, 13 of them its 84 MB at the copy's
+//                  rate; about 4 us are launch, first loads and epilogue, and 120 of 148 SMs have a part.
+//   small K        the epilogue: 802 x 12944 x 128 15.7 us, 21 MB of y.
+// The issuing warps run their loops as whole warps with one elected lane: run by a lane alone the same loops took
+// 380 ns a k-tile, more than the loads (29 us for the single token).
+//
 // Every wait is bounded; one that runs out sets the context's operator error word, and an abort flag that
 // ends the other roles' waits.
 #include <cuda.h>  // CUtensorMap

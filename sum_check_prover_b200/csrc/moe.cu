@@ -28,7 +28,9 @@ namespace {
 // same expert are found by match.any and take the ranks after the histogram's count in the order of the
 // lanes, so the sort is stable. The histograms' prefix sums (over a block's warps, then over the cluster's
 // blocks through distributed shared memory, then over the experts) give every warp its first row of each
-// expert, which a second pass over the run adds to the ranks.
+// expert, which a second pass over the run adds to the ranks. Bound by latency: 8 choices take 2.9 us, 16382
+// of 128 experts 7.6, 65536 15 (0.5 MB, 0.1 us of memory traffic; a launch alone is about 2 us). No block waits
+// for another but at the cluster's barriers, and nothing is kept in memory between calls.
 constexpr int MS_HIST_BYTES = 176 * 1024;
 constexpr int MS_MAX_CLUSTER = 8;
 
@@ -149,6 +151,9 @@ __global__ void __launch_bounds__(1024)
 
 constexpr int MO_CHOICES = 4;  // positions (and weights) of a token kept in registers at a time
 
+// Bound by HBM: 8192 x 5120 bf16 to two rows each, 252 MB, takes 41.7 us, 6.0 TB/s (a plain copy here: 6.4).
+// A token's row is read once and written k times, so nothing but the positions is read twice.
+//
 // rows[pos[t][j]] = x[t] in units of A bytes; one token per tpr threads, blockIdx.y a share of the columns. U
 // loads of a thread are in flight before its stores. ANY: x from any address.
 template <int A, int U, bool ANY>
@@ -200,6 +205,9 @@ void launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, i
 
 // ---- combine --------------------------------------------------------------------------------
 
+// Bound by HBM: 8192 x 5120 bf16, k = 2, 252 MB, takes 43.3 us, 5.8 TB/s (k = 1: 35 us, 4.8: a block waits for its
+// position before its one load a thread); fp32 rows of the odd width 4099, k = 2, 403 MB, 74 us, 5.4 TB/s.
+//
 // out[t] = base[t] + sum_j w[t][j] rows[pos[t][j]] in fp32, rounded once; V elements per load (ANY: from any
 // address), U vectors of a thread at a time
 template <typename RT, typename OT, int V, int U, bool ANY>
@@ -260,6 +268,8 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
 
 constexpr int MO_GRAD_THREADS = 512;
 
+// Bound by HBM: 8192 x 5120 bf16, k = 2, 420 MB, takes 68 us, 6.2 TB/s.
+//
 // One token per tpr threads: its k rows' gradients and the k inner products (fp32, a fixed order: a
 // thread's columns, its warp's tree, then the warps). Two choices at a time read dout once; blockIdx.y a
 // share of the choices. ANY: loads from any address.

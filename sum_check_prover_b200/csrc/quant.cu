@@ -10,6 +10,9 @@
 //
 // A row with a NaN or an infinity has no scale: its scale is NaN and its integers are 0, so every
 // product with it is NaN. A row of zeros has scale 0.
+// One read of the row: it stays in registers between the maximum and the integers. 8192 x 5120 bf16 into
+// experts' rows, 126 MB, takes 26 us, 4.8 TB/s: ten rows of 10 KB are in flight on an SM (64 registers a thread),
+// each for about 4.5 us, and that wait bounds it (fewer registers spill: 31 us at 48).
 #include <algorithm>
 
 #include "fp_ops.cuh"
