@@ -789,8 +789,9 @@ int fp_quantize_rows(fp_ctx* ctx, const void* x, int x_type, int64_t T, int64_t 
  *  y        N rows of M values of y_type, pitch ldy.
  * 1 <= M <= 2^24, 0 <= N <= 2^24, 1 <= K < 2^17 (exact int32 sums), 1 <= E <= 4096, E M < 2^31 - 255.
  * Fastest when w, x, ldw and ldx are multiples of 16. An operand whose address or pitch is not is first
- * copied (the experts that have rows) to rows that are, in stream-ordered memory of the context, which
- * keeps it for later calls (FP_ERR_OOM if there is none); inside a graph it is the graph's. The kernel's waits are bounded: should one run
+ * copied (of weights the experts that have rows; none where few tokens meet them) to rows that are, in
+ * stream-ordered memory of the context, which keeps it for later calls (FP_ERR_OOM if there is none);
+ * inside a graph it is the graph's. The kernel's waits are bounded: should one run
  * out, the next call on the context returns FP_ERR_TIMEOUT (once) and the earlier y is not valid.
  */
 int fp_matmul_i8(fp_ctx* ctx, const int8_t* w, int64_t ldw, const float* w_scale, int E, int64_t M, int64_t K,

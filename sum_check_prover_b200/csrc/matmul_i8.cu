@@ -72,6 +72,17 @@ struct alignas(64) MiArgs {
     volatile uint64_t* err;
 };
 
+// (CLASSES) Weights whose pitch is no multiple of 16: the rows whose number is c modulo C, C = 16 / gcd(pitch, 16),
+// lie C pitches apart, a multiple of 16, and begin at the same byte s_c of 16. Each such class is a matrix that TMA
+// can read, its rows s_c bytes to the right; a tile is of one class and meets tokens shifted as far (C copies of
+// the tokens, zeros around them, which also cancel what the class's rows have before and after K).
+constexpr int MI_MAX_CLASSES = 16;
+struct alignas(64) MiClassArgs : MiArgs {
+    CUtensorMap wc[MI_MAX_CLASSES];
+    int32_t classes, per_class;  // C; tiles of an expert's rows of one class
+    int32_t box;                 // rows of a tile at most
+};
+
 __device__ __forceinline__ uint32_t mi_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 // K-major operand with the 128-byte swizzle: 8-row x 128-byte atoms 1024 bytes apart. The low word holds
@@ -260,10 +271,33 @@ __device__ __forceinline__ void mi_put(const MiArgs& a, const int32_t (&v)[C], c
         mi_store<__nv_bfloat16>(a, v, xs, n, cols, m0, ws, (__nv_bfloat16*)buf, lane);
 }
 
-template <int BN, bool SPLIT, bool PAIR>
+// the same for channels that lie apart: single values, m the lane's channel
+template <typename YT>
+__device__ __forceinline__ void mi_store_apart(const MiArgs& a, const int32_t (&v)[16], const float* xs, int64_t n, int cols,
+                                               int64_t m, float ws, bool live) {
+    if (!live || m >= a.M) return;
+    YT* y = reinterpret_cast<YT*>(a.y) + n * a.ldy + m;
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+        if (i < cols) y[i * a.ldy] = fp_from_f<YT>((float)v[i] * xs[i] * ws);
+}
+__device__ __forceinline__ void mi_put_apart(const MiArgs& a, const int32_t (&v)[16], const float* xs, int64_t n, int cols,
+                                             int64_t m, float ws, bool live) {
+    if (a.y_type == FP_F32)
+        mi_store_apart<float>(a, v, xs, n, cols, m, ws, live);
+    else if (a.y_type == FP_F16)
+        mi_store_apart<__half>(a, v, xs, n, cols, m, ws, live);
+    else
+        mi_store_apart<__nv_bfloat16>(a, v, xs, n, cols, m, ws, live);
+}
+
+// (CLASSES) the place in class c of the first of its rows from row g on
+__device__ __forceinline__ int mi_class_row(int g, int c, int classes) { return (g - c + classes - 1) / classes; }
+
+template <int BN, bool SPLIT, bool PAIR, bool CLASSES>
 __global__ void __launch_bounds__(MI_THREADS, 1)
-    matmul_i8_kernel(const __grid_constant__ MiArgs a) {
-    static_assert(!(PAIR && SPLIT), "a pair has a tile's whole K");
+    matmul_i8_kernel(const __grid_constant__ std::conditional_t<CLASSES, MiClassArgs, MiArgs> a) {
+    static_assert(!(PAIR && SPLIT) && !(CLASSES && (PAIR || SPLIT)), "a pair and a class have a tile's whole K");
     constexpr int XB = mi_box_rows(BN), XROWS = PAIR ? BN / 2 : BN;  // token rows of a box, of this block's stage
     constexpr int STAGE = MI_W_BYTES + XROWS * MI_BK;
     constexpr int TM = PAIR ? 2 * MI_BM : MI_BM;  // channels of a tile
@@ -322,7 +356,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
     // read (with plain loads: an invariant one could be moved up across the wait). The next kernel may be brought
     // onto the SMs that this one leaves.
     if (warp == 0 && lane == 0) {
-        asm volatile("prefetch.tensormap [%0];\n" ::"l"(&a.tw) : "memory");
+        if (!CLASSES) asm volatile("prefetch.tensormap [%0];\n" ::"l"(&a.tw) : "memory");
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(&a.tx) : "memory");
     }
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -406,9 +440,18 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
             const MiTokens tk = mi_tokens(first, tiles, a.E, u);
             // PAIR: half of the MMA's columns each, and both blocks' bytes awaited by the issuing block
             const int half = PAIR ? mi_columns<PAIR>(tk.cols) >> 1 : 0;
-            const int boxes = ((PAIR ? half : tk.cols) + XB - 1) / XB, xrow = tk.n0 + (PAIR ? (int)crank * half : 0);
-            const uint32_t bytes = MI_W_BYTES + boxes * XB * MI_BK;
-            const int wrow = tk.e * a.M + m * TM + wlead;
+            const int boxes = ((PAIR ? half : tk.cols) + XB - 1) / XB;
+            int xrow = tk.n0 + (PAIR ? (int)crank * half : 0);
+            uint32_t bytes = MI_W_BYTES + boxes * XB * MI_BK;
+            int wrow = tk.e * a.M + m * TM + wlead;
+            const CUtensorMap* tw = &a.tw;
+            if constexpr (CLASSES) {
+                const int cls = m / a.per_class;
+                wrow = mi_class_row(tk.e * a.M, cls, a.classes) + (m - cls * a.per_class) * a.box;
+                xrow += cls * a.N;
+                tw = &a.wc[cls];
+                bytes = (uint32_t)a.box * MI_BK + boxes * XB * MI_BK;
+            }
             for (int kt = kt0; kt < kt1; kt++) {
                 if (!mi_wait_warp(empty0 + 8 * s, ph, &s_abort, err)) {
                     ok = false;
@@ -420,7 +463,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(full0 + 8 * s),
                                      "r"(PAIR ? 2 * bytes : bytes)
                                      : "memory");
-                    mi_tma<PAIR>(dst, &a.tw, kt * MI_BK, wrow, fb);
+                    mi_tma<PAIR>(dst, tw, kt * MI_BK, wrow, fb);
 #pragma unroll
                     for (int b = 0; b < XROWS / XB; b++)
                         if (b < boxes)
@@ -504,8 +547,16 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
                 continue;
             }
             const int part = alone ? 0 : group, step = alone ? 16 : 32;
-            const int64_t m0 = (int64_t)m * TM + wlead + 32 * qd;  // the warp's first channel
-            const float ws = m0 + lane < a.M ? a.w_scale[(int64_t)tk.e * a.M + m0 + lane] : 0.0f;
+            int64_t m0 = (int64_t)m * TM + wlead + 32 * qd;  // the warp's first channel
+            int stride = 1, rows = 32;                       // the channels' distance, how many are the tile's
+            if constexpr (CLASSES) {
+                const int cls = m / a.per_class, at = (m - cls * a.per_class) * a.box;
+                stride = a.classes;
+                m0 = cls + (int64_t)stride * (mi_class_row(tk.e * a.M, cls, stride) + at + 32 * qd) - (int64_t)tk.e * a.M;
+                rows = a.box - 32 * qd;
+            }
+            const int64_t mine = m0 + (int64_t)stride * lane;
+            const float ws = lane < rows && mine < a.M ? a.w_scale[(int64_t)tk.e * a.M + mine] : 0.0f;
             // the scales of this warp's tokens, before their sums are there: chunk i of 16 columns at 16 i (SPLIT:
             // all columns, for the share may lie anywhere)
             float* xs = s_scale[warp - 2];
@@ -529,6 +580,10 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
 #pragma unroll 1
                 for (; c0 < tk.cols; c0 += step) {
                     if (c0 + step < tk.cols) mi_ld16(base + (uint32_t)(c0 + step), nx);
+                    if constexpr (CLASSES)
+                        mi_put_apart(a, v, xs + (alone ? c0 : (c0 >> 5) * 16), (int64_t)tk.n0 + c0, min(16, tk.cols - c0), mine,
+                                     ws, lane < rows);
+                    else
                     mi_put<16>(a, v, xs + (alone ? c0 : (c0 >> 5) * 16), (int64_t)tk.n0 + c0, min(16, tk.cols - c0), m0, ws, s_out[warp - 2], lane);
                     mi_ld_wait();
 #pragma unroll
@@ -611,117 +666,186 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
 //
 // TMA wants an address and a pitch that are multiples of 16. Rows that are not so are first copied to rows
 // that are, in stream-ordered memory from the context's pool (inside a graph its own allocation nodes), by
-// one pass: a thread loads the two aligned 16 bytes that its own lie in and shifts. An expert without tokens is
-// passed over. (Realigning inside the product, with warps that
-// load words into the swizzled stages, took 1224 us on 2352 x 9600 x 7454: every tile of channels did the
-// tokens' rows again.)
+// one launch for both operands: a thread loads the two aligned 16 bytes that its own lie in and shifts. An expert
+// without tokens is passed over. Weights that few tokens meet are not copied but read by classes of rows
+// (MiClassArgs): then only the tokens are copied, shifted for every class.
+// (Realigning inside the product, with warps that load words into the swizzled stages, took 1224 us on 2352 x 9600 x
+// 7454 where this takes 188: every tile of channels did the tokens' rows again.)
 
 struct MiOperand {
     const int8_t* p;
     int64_t ld, rows;
 };
 
-// rows of K bytes at src (pitch ld) to dst (pitch 16 chunks); the last bytes of a pitch are 0. One thread per
-// 16 bytes, MI_RE of them a block's width apart. M: rows of an expert, with offsets.
-constexpr int MI_RE = 4;
-__global__ void __launch_bounds__(256)
-    realign_rows_kernel(const int8_t* __restrict__ src, int64_t ld, int64_t rows, int K, int8_t* __restrict__ dst,
-                        int chunks, const int32_t* __restrict__ offsets, int M) {
-    const int64_t at0 = (int64_t)blockIdx.x * (256 * MI_RE);
-    const int64_t row0 = at0 / chunks;
-    const int c0 = (int)(at0 % chunks);
-    const FpSpan span = fp_span(src, rows, ld, K);
+// rows of K bytes at src (pitch ld), `copies` times, copy c shifted right by (c step) mod 16 bytes, to rows of
+// 16 chunks bytes; zeros around them. M: rows of an expert, with offsets.
+struct MiRealign {
+    const int8_t* src;
+    int8_t* dst;
+    int64_t ld;
+    const int32_t* offsets;
+    uint32_t rows, blocks;         // rows of a copy; blocks of the job
+    uint32_t chunks, per, across;  // 16-byte pieces of a row, rows of a block, blocks across a row
+    int32_t copies, step, M;
+};
+constexpr int MI_RE = 4;  // 16-byte pieces of a thread, a block's width apart
+
+__global__ void __launch_bounds__(256) realign_rows_kernel(MiRealign j0, MiRealign j1, int K) {
+    const bool second = blockIdx.x >= j0.blocks;
+    const MiRealign j = second ? j1 : j0;
+    const uint32_t b = blockIdx.x - (second ? j0.blocks : 0), down = b / j.across, c0 = (b - down * j.across) * (256 * MI_RE);
+    const FpSpan span = fp_span(j.src, j.rows, j.ld, K);
 #pragma unroll
     for (int u = 0; u < MI_RE; u++) {
-        const uint32_t i = (uint32_t)c0 + threadIdx.x + 256 * u;
-        const int64_t row = row0 + i / (uint32_t)chunks;
-        const int c = (int)(i % (uint32_t)chunks);
-        if (row >= rows) break;
-        if (offsets) {
-            const int e = (int)(row / M);
-            if (__ldg(offsets + e + 1) <= max(0, __ldg(offsets + e))) continue;
+        // a block has several short rows, or a part of a long one
+        const uint32_t i = c0 + threadIdx.x + 256 * u, r = j.across == 1 ? i / j.chunks : 0, c = i - r * j.chunks;
+        const uint32_t out = down * j.per + r;
+        if (r >= j.per || c >= j.chunks || out >= j.rows * j.copies) break;
+        uint32_t row = out;
+        int first = 16 * (int)c;  // the K index of the piece's first byte
+        if (j.copies > 1) {
+            const uint32_t copy = out / j.rows;
+            row = out - copy * j.rows;
+            first -= (int)(copy * j.step) & 15;
         }
-        const int8_t* p = src + row * ld + 16 * (int64_t)c;
-        const int valid = K - 16 * c;
+        if (j.offsets) {
+            const uint32_t e = row / (uint32_t)j.M;
+            if (__ldg(j.offsets + e + 1) <= max(0, __ldg(j.offsets + e))) continue;
+        }
+        const int8_t* p = j.src + (int64_t)row * j.ld + first;
+        const int lo = max(0, -first), hi = K - first;  // the bytes of the piece inside the row
         FpWords<16> w;
         uint32_t o[4];
-        if (fp_load16_any(p, span, o)) {
+        if (hi <= lo) {
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int left = valid - 4 * j;
-                w.w[j] = o[j] & (left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1);
+            for (int q = 0; q < 4; q++) w.w[q] = 0;
+        } else if (fp_load16_any(p, span, o)) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int a = lo - 4 * q, b = hi - 4 * q;
+                w.w[q] = o[q] & (b >= 4 ? 0xFFFFFFFFu : b <= 0 ? 0u : (1u << (8 * b)) - 1) &
+                         (a <= 0 ? 0xFFFFFFFFu : a >= 4 ? 0u : ~((1u << (8 * a)) - 1));
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                w.w[j] = 0;
+            for (int q = 0; q < 4; q++) {
+                w.w[q] = 0;
 #pragma unroll
                 for (int b = 0; b < 4; b++)
-                    if (4 * j + b < valid) w.w[j] |= (uint32_t)(uint8_t)p[4 * j + b] << (8 * b);
+                    if (4 * q + b >= lo && 4 * q + b < hi) w.w[q] |= (uint32_t)(uint8_t)p[4 * q + b] << (8 * b);
             }
         }
-        w.store(dst + (row * chunks + c) * 16);
+        w.store(j.dst + ((int64_t)out * j.chunks + c) * 16);
     }
 }
 
 // Scratch rows of a call, given back to the pool in the order of the stream when the call has queued its work
 struct MiScratch {
     cudaStream_t st;
-    int8_t* p[2] = {nullptr, nullptr};
+    int8_t* p = nullptr;
     explicit MiScratch(cudaStream_t s) : st(s) {}
     ~MiScratch() {
-        for (int8_t* q : p)
-            if (q) cudaFreeAsync(q, st);
+        if (p) cudaFreeAsync(p, st);
     }
     MiScratch(const MiScratch&) = delete;
     MiScratch& operator=(const MiScratch&) = delete;
 };
 
-// makes the operand readable for TMA
-int mi_realign(fp_ctx* c, MiOperand& o, int K, const int32_t* offsets, int M, int8_t** scratch, cudaStream_t st) {
-    if (((uintptr_t)o.p | (uint64_t)o.ld) % 16 == 0) return FP_OK;
-    const int64_t dld = (K + 15) & ~15;
-    if (!c->pool) return fp_fail(c, FP_ERR_OOM, "fp_matmul_i8: no memory pool for realigned rows on this device");
-    const cudaError_t e = cudaMallocFromPoolAsync((void**)scratch, (size_t)dld * o.rows, c->pool, st);
-    if (e != cudaSuccess) {
-        *scratch = nullptr;
-        cudaGetLastError();
-        return fp_fail(c, FP_ERR_OOM, std::string("fp_matmul_i8: ") + std::to_string((size_t)dld * o.rows) +
-                                          " bytes for realigned rows: " + cudaGetErrorString(e));
+bool mi_readable(const MiOperand& o) { return ((uintptr_t)o.p | (uint64_t)o.ld) % 16 == 0; }
+
+// makes both operands readable for TMA; classes > 0: only the tokens are copied, for so many classes of weight rows
+int mi_realign(fp_ctx* c, MiOperand& w, MiOperand& x, int K, const int32_t* offsets, int M, int classes, MiScratch& scratch) {
+    MiOperand* op[2] = {!classes && !mi_readable(w) ? &w : nullptr, classes || !mi_readable(x) ? &x : nullptr};
+    if (!op[0] && !op[1]) return FP_OK;
+    MiRealign job[2] = {};
+    size_t bytes = 0, at[2] = {0, 0};
+    int64_t blocks = 0;
+    for (int i = 0; i < 2; i++) {
+        if (!op[i]) continue;
+        MiRealign& j = job[i];
+        j.src = op[i]->p, j.ld = op[i]->ld, j.rows = (uint32_t)op[i]->rows, j.M = M;
+        j.copies = i == 1 && classes ? classes : 1;
+        j.step = i == 1 && classes ? (int)(w.ld & 15) : 0;
+        j.chunks = (uint32_t)(K + (j.copies > 1 ? 15 : 0) + 15) / 16;
+        j.offsets = i == 0 ? offsets : nullptr;
+        j.per = std::max(1u, 256 * MI_RE / j.chunks);
+        j.across = (j.chunks + 256 * MI_RE - 1) / (256 * MI_RE);
+        const int64_t n = ((int64_t)j.rows * j.copies + j.per - 1) / j.per * j.across;
+        j.blocks = (uint32_t)n;
+        at[i] = bytes;
+        bytes += (size_t)16 * j.chunks * j.rows * j.copies;
+        blocks += n;
     }
-    const int chunks = (int)(dld / 16);
-    const int64_t blocks = (o.rows * chunks + 256 * MI_RE - 1) / (256 * MI_RE);
-    if (blocks > 0x7fffffffll) return fp_fail(c, FP_ERR_SHAPE, "fp_matmul_i8: an operand of over 2^45 bytes with an odd pitch");
+    if (blocks > 0x7fffffffll) return fp_fail(c, FP_ERR_SHAPE, "fp_matmul_i8: operands of over 2^45 bytes with odd pitches");
+    if (!c->pool) return fp_fail(c, FP_ERR_OOM, "fp_matmul_i8: no memory pool for realigned rows on this device");
+    const cudaError_t e = cudaMallocFromPoolAsync((void**)&scratch.p, bytes, c->pool, scratch.st);
+    if (e != cudaSuccess) {
+        scratch.p = nullptr;
+        cudaGetLastError();
+        return fp_fail(c, FP_ERR_OOM,
+                       std::string("fp_matmul_i8: ") + std::to_string(bytes) + " bytes for realigned rows: " + cudaGetErrorString(e));
+    }
+    for (int i = 0; i < 2; i++) {
+        if (!op[i]) continue;
+        job[i].dst = scratch.p + at[i];
+        op[i]->p = job[i].dst, op[i]->ld = 16 * (int64_t)job[i].chunks, op[i]->rows *= job[i].copies;
+    }
     int slot;
-    fp_op_tic(c, st, K_REALIGN, 2.0 * (double)K * o.rows, &slot);
-    realign_rows_kernel<<<(unsigned)blocks, 256, 0, st>>>(o.p, o.ld, o.rows, K, *scratch, chunks, offsets, M);
-    fp_toc(c, st, slot);
+    fp_op_tic(c, scratch.st, K_REALIGN, 2.0 * (double)bytes, &slot);
+    realign_rows_kernel<<<(unsigned)blocks, 256, 0, scratch.st>>>(job[0], job[1], K);
+    fp_toc(c, scratch.st, slot);
     FP_CUDA(c, cudaGetLastError());
-    o.p = *scratch;
-    o.ld = dld;
     return FP_OK;
 }
 
-template <int BN, bool SPLIT, bool PAIR>
-constexpr int mi_kernel_bit() {
-    return 1 + (BN == 32 ? 0 : BN == 128 ? 4 : 8) + 2 * SPLIT + PAIR;
+// Classes of weight rows to read apart (0: none). Where a group has up to 128 rows and the shifted copies of the
+// tokens are at most a quarter of the weights that need no copy: 64 experts of 4512 x 13885 over 1087 tokens take
+// 873 us and took 2426 with copied weights, 8192 x 5121 for 64 tokens 27 and 38. The copied rows win where many
+// tokens meet each weight: 4096 x 4097 for 128 tokens 34 and 27.
+int mi_classes(const MiOperand& w, int64_t E, int64_t M, int64_t N, int64_t rows) {
+    if (mi_readable(w) || (uintptr_t)w.p % 16 != 0 || rows > 128) return 0;
+    int classes = 16;
+    while (classes > 2 && (uint64_t)w.ld * (classes / 2) % 16 == 0) classes /= 2;
+    return M >= 4 * classes && classes * N <= std::min(E, N) * M / 4 ? classes : 0;
 }
 
-template <int BN, bool SPLIT, bool PAIR>
-int launch_mi(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x, int64_t token_tiles, int split, cudaStream_t st) {
+template <int BN, bool SPLIT, bool PAIR, bool CLASSES>
+constexpr int mi_kernel_bit() {
+    return CLASSES ? 13 : 1 + (BN == 32 ? 0 : BN == 128 ? 4 : 8) + 2 * SPLIT + PAIR;
+}
+
+template <int BN, bool SPLIT, bool PAIR, bool CLASSES = false>
+int launch_mi(fp_ctx* c, std::conditional_t<CLASSES, MiClassArgs, MiArgs>& a, const MiOperand& w, const MiOperand& x,
+              int64_t token_tiles, int split, cudaStream_t st) {
     constexpr int STAGE = MI_W_BYTES + (PAIR ? BN / 2 : BN) * MI_BK;
     constexpr int TM = PAIR ? 2 * MI_BM : MI_BM;
     const int cluster = PAIR ? 2 : split;
-    if (!fp_tmap_u8_2d(&a.tw, w.p, (uint64_t)a.K, (uint64_t)w.rows, (uint64_t)w.ld, MI_BK, MI_BM, true) ||
-        !fp_tmap_u8_2d(&a.tx, x.p, (uint64_t)a.K, (uint64_t)x.rows, (uint64_t)x.ld, MI_BK, mi_box_rows(BN), true))
+    if constexpr (CLASSES) {
+        a.box = (int32_t)std::min<int64_t>(MI_BM, ((a.M + a.classes - 1) / a.classes + 7) / 8 * 8);
+        a.per_class = (int32_t)(((a.M + a.classes - 1) / a.classes + a.box - 1) / a.box);
+        a.mt = a.classes * a.per_class;
+        for (int i = 0; i < a.classes; i++) {
+            const int64_t at = i * w.ld;  // (the first row of the class, and the bytes before it that align it)
+            const int s = (int)(at & 15);
+            if (i < w.rows &&
+                !fp_tmap_u8_2d(&a.wc[i], w.p + at - s, (uint64_t)(s + a.K), (uint64_t)((w.rows - i + a.classes - 1) / a.classes),
+                               (uint64_t)(a.classes * w.ld), MI_BK, (uint32_t)a.box, true))
+                return fp_fail(c, FP_ERR_CUDA, "fp_matmul_i8: tensor map encoding failed");
+        }
+    } else {
+        if (!fp_tmap_u8_2d(&a.tw, w.p, (uint64_t)a.K, (uint64_t)w.rows, (uint64_t)w.ld, MI_BK, MI_BM, true))
+            return fp_fail(c, FP_ERR_CUDA, "fp_matmul_i8: tensor map encoding failed");
+        a.mt = (a.M + TM - 1) / TM;
+    }
+    // (classes: the whole of a shifted row)
+    if (!fp_tmap_u8_2d(&a.tx, x.p, (uint64_t)(CLASSES ? x.ld : a.K), (uint64_t)x.rows, (uint64_t)x.ld, MI_BK, mi_box_rows(BN), true))
         return fp_fail(c, FP_ERR_CUDA, "fp_matmul_i8: tensor map encoding failed");
-    a.mt = (a.M + TM - 1) / TM;
     a.per = SPLIT ? (((BN + split - 1) / split) + 7) & ~7 : 0;
     const size_t extra = (SPLIT ? (size_t)split * a.per * MI_BM * 4 : 0) + 8 * ((size_t)a.E + 1) + 1024;
     a.stages = (int)std::min<size_t>(MI_MAX_STAGES, (MI_SMEM - extra) / STAGE);
     if (extra + 2 * STAGE > (size_t)MI_SMEM) return fp_fail(c, FP_ERR_SHAPE, "fp_matmul_i8: too many experts");  // (never: 3 stages at E = 4096)
-    auto kern = matmul_i8_kernel<BN, SPLIT, PAIR>;
-    FP_CUDA(c, fp_op_smem(c, mi_kernel_bit<BN, SPLIT, PAIR>(), kern, MI_SMEM));
+    auto kern = matmul_i8_kernel<BN, SPLIT, PAIR, CLASSES>;
+    FP_CUDA(c, fp_op_smem(c, mi_kernel_bit<BN, SPLIT, PAIR, CLASSES>(), kern, MI_SMEM));
     const int64_t tiles = token_tiles * a.mt;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(cluster * (SPLIT ? tiles : std::min<int64_t>(tiles, c->num_sms / cluster))));
@@ -745,8 +869,8 @@ template <int BN>
 int64_t mi_clusters(fp_ctx* c, int split) {
     int16_t& n = c->op_clusters[BN == 32 ? 0 : 1][split];
     if (n == 0) {
-        auto kern = matmul_i8_kernel<BN, true, false>;
-        if (fp_op_smem(c, mi_kernel_bit<BN, true, false>(), kern, MI_SMEM) != cudaSuccess) return 0;
+        auto kern = matmul_i8_kernel<BN, true, false, false>;
+        if (fp_op_smem(c, mi_kernel_bit<BN, true, false, false>(), kern, MI_SMEM) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)split);
         cfg.blockDim = dim3(MI_THREADS);
@@ -835,21 +959,27 @@ int fp_matmul_i8(fp_ctx* c, const int8_t* w, int64_t ldw, const float* w_scale, 
     cudaStream_t st = (cudaStream_t)stream;
     if (N == 1) ldx = (K + 15) & ~15ll, ldy = M;  // a single row has no pitch: one that keeps its alignment
     if (E * M == 1) ldw = (K + 15) & ~15ll;
+    // rows of a group: N of a dense product, twice the mean of those that can have rows by expert
+    const int64_t rows = E == 1 ? N : 2 * ((N + std::min<int64_t>(E, N) - 1) / std::min<int64_t>(E, N));
     MiOperand ow{w, ldw, E * M}, ox{x, ldx, N};
+    const int classes = mi_classes(ow, E, M, N, rows);
     MiScratch scratch(st);
-    int rc = mi_realign(c, ow, (int)K, E > 1 ? offsets : nullptr, (int)M, &scratch.p[0], st);
-    if (!rc) rc = mi_realign(c, ox, (int)K, nullptr, 1, &scratch.p[1], st);
+    int rc = mi_realign(c, ow, ox, (int)K, E > 1 ? offsets : nullptr, (int)M, classes, scratch);
     if (rc) return rc;
-    MiArgs a = {};
+    MiClassArgs a = {};
     a.w_scale = w_scale, a.x_scale = x_scale, a.offsets = offsets, a.y = y, a.ldy = ldy;
     a.M = (int32_t)M, a.K = (int32_t)K, a.N = (int32_t)N, a.E = E, a.y_type = y_type;
     a.yvec = (M * ys) % 16 == 0 && fp_common_align({(uint64_t)(uintptr_t)y, (uint64_t)ldy * ys}) == 16;
     a.err = &c->mb_dev->op_err;
-    // rows of a group: N of a dense product, twice the mean of those that can have rows by expert
-    const int64_t rows = E == 1 ? N : 2 * ((N + std::min<int64_t>(E, N) - 1) / std::min<int64_t>(E, N));
+    a.classes = classes;
     int slot;
     fp_op_tic(c, st, K_MATMUL_I8, (double)std::min<int64_t>(E, N) * M * K + (double)N * (K + ys * (double)M), &slot);
-    rc = launch_product(c, a, ow, ox, rows, st);
+    if (classes) {
+        a.nk = (int32_t)((K + 15 + MI_BK - 1) / MI_BK);
+        rc = launch_mi<128, false, false, true>(c, a, ow, ox, mi_token_tiles(a, 128), 1, st);
+    } else {
+        rc = launch_product(c, a, ow, ox, rows, st);
+    }
     fp_toc(c, st, slot);
     return rc;
 }

@@ -756,6 +756,37 @@ def test_odd_pitches_in_graphs(env):
             assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("K", [65, 130, 268, 1032, 2047])  # pitches of 1, 2, 4, 8 and 15 modulo 16
+@pytest.mark.parametrize("M", [64, 100, 1031, 2500])
+@pytest.mark.parametrize("counts", [None, [1, 0, 3, 40], [0, 2, 0, 0, 1], [5]])
+def test_weights_with_odd_pitches_and_few_tokens(env, K, M, counts):
+    # weights read by classes of rows that begin at the same byte of 16, tokens shifted for each
+    torch, fp, ctx = env
+    E = 0 if counts is None else len(counts)
+    N = 2 if counts is None else sum(counts) + 1
+    w, x, ws, xs, y, yb = product_case(torch, N, M, K, E, "float32", K + M, pady=1)
+    y.fill_(7)
+    before = yb.clone()
+    if E == 0:
+        ctx.matmul_i8(w, x, y, ws, xs)
+        check_product(torch, w, x, ws, xs, y)
+    else:
+        ends = np.concatenate([[0], np.cumsum(counts)])
+        ctx.matmul_i8(w, x, y, ws, xs, offsets=torch.from_numpy(ends.astype(np.int32)).cuda())
+        check_product(torch, w, x, ws, xs, y, ends)
+        assert bool((y[ends[-1]:] == 7).all())
+    untouched(torch, y, yb, before)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("padw,lead", [(3, 0), (8, 0), (1, 5), (0, 3)])
+def test_weight_views_with_odd_pitches(env, dtype, padw, lead):
+    torch, fp, ctx = env
+    w, x, ws, xs, y, yb = product_case(torch, 7, 900, 640 if padw else 643, 0, dtype, 60, padw=padw, lead=lead)
+    ctx.matmul_i8(w, x, y, ws, xs)
+    check_product(torch, w, x, ws, xs, y)
+
+
 def test_odd_pitches_by_expert(env):
     # experts without rows are not realigned; falling offsets do not hide one that has rows
     torch, fp, ctx = env
