@@ -771,7 +771,7 @@ enum { FP_F32 = 0, FP_F16 = 1, FP_BF16 = 2 }; /* types of real values */
  *  pos    nullable. Null: token t's row is row t of q and scale (R >= T). Else T x k int32: token t
  *         is written to rows pos[t][j] for every j < k; positions outside [0, R) are passed over.
  *  q      R rows of K, pitch ldq. scale: R. Rows that no token goes to are left as they were.
- * 0 <= T <= 2^24, 1 <= K <= 2^20, 0 <= R < 2^31, T k < 2^31.
+ * 0 <= T <= 2^24, 1 <= K <= 2^20, 0 <= R < 2^31, k >= 1 and T k < 2^31 with pos.
  */
 int fp_quantize_rows(fp_ctx* ctx, const void* x, int x_type, int64_t T, int64_t K, int64_t ldx, const int32_t* pos,
                      int k, int64_t R, int8_t* q, int64_t ldq, float* scale, void* stream);
@@ -810,7 +810,7 @@ int fp_moe_sort(fp_ctx* ctx, const int32_t* e, int64_t n, int E, int32_t* offset
  * Rows to their experts: rows[pos[t][j]] = x[t] for every j < k; positions outside [0, R) are passed
  * over and rows that no token goes to are left as they were. Rows are bytes of any type: row_bytes of
  * them, pitches ldx and ldr in bytes. Its gradient is fp_moe_combine without weights.
- * 0 <= T <= 2^24, T k < 2^31, 0 <= R < 2^31, 1 <= row_bytes <= 2^24.
+ * 0 <= T <= 2^24, k >= 1, T k < 2^31, 0 <= R < 2^31, 1 <= row_bytes <= 2^24.
  */
 int fp_moe_dispatch(fp_ctx* ctx, const void* x, int64_t T, int64_t row_bytes, int64_t ldx, const int32_t* pos, int k,
                     int64_t R, void* rows, int64_t ldr, void* stream);
@@ -820,7 +820,7 @@ int fp_moe_dispatch(fp_ctx* ctx, const void* x, int64_t T, int64_t row_bytes, in
  * in fp32 in the order of j and rounded once; positions outside [0, R) add nothing.
  *  weights  nullable (all 1): T x k fp32.   base  nullable (0): T rows of M of out_type, pitch ldb, for
  *           instance a shared expert's output; base may be out.
- * 0 <= T <= 2^24, T k < 2^31, 0 <= R < 2^31, 1 <= M <= 2^24.
+ * 0 <= T <= 2^24, k >= 1, T k < 2^31, 0 <= R < 2^31, 1 <= M <= 2^24.
  */
 int fp_moe_combine(fp_ctx* ctx, const void* rows, int rows_type, int64_t R, int64_t ldr, const int32_t* pos,
                    const float* weights, const void* base, int64_t ldb, int64_t T, int k, int64_t M, void* out,

@@ -527,7 +527,11 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
             mi_drain(mi_smem(&fin), 0);
         }
         __syncwarp();
-    } else if (warp >= 2) {
+    } else if (warp == 1) {
+        // ---- (PAIR) the second block stays until the last of the first one's arrivals at its barriers ----
+        if (lane == 0) mi_drain(mi_smem(&fin), 0);
+        __syncwarp();
+    } else {
         // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31; the two warps of the same lanes take every
         // other chunk of 16 columns of a tile, or, of tiles with few columns, whose time is mostly the way to
         // the scales and back, every other tile. A chunk's load is in flight while the one before is stored
@@ -580,11 +584,12 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
 #pragma unroll 1
                 for (; c0 < tk.cols; c0 += step) {
                     if (c0 + step < tk.cols) mi_ld16(base + (uint32_t)(c0 + step), nx);
+                    const float* sc = xs + (alone ? c0 : (c0 >> 5) * 16);
+                    const int cols = min(16, tk.cols - c0);
                     if constexpr (CLASSES)
-                        mi_put_apart(a, v, xs + (alone ? c0 : (c0 >> 5) * 16), (int64_t)tk.n0 + c0, min(16, tk.cols - c0), mine,
-                                     ws, lane < rows);
+                        mi_put_apart(a, v, sc, (int64_t)tk.n0 + c0, cols, mine, ws, lane < rows);
                     else
-                    mi_put<16>(a, v, xs + (alone ? c0 : (c0 >> 5) * 16), (int64_t)tk.n0 + c0, min(16, tk.cols - c0), m0, ws, s_out[warp - 2], lane);
+                        mi_put<16>(a, v, sc, (int64_t)tk.n0 + c0, cols, m0, ws, s_out[warp - 2], lane);
                     mi_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; i++) v[i] = nx[i];
@@ -837,13 +842,14 @@ int launch_mi(fp_ctx* c, std::conditional_t<CLASSES, MiClassArgs, MiArgs>& a, co
             return fp_fail(c, FP_ERR_CUDA, "fp_matmul_i8: tensor map encoding failed");
         a.mt = (a.M + TM - 1) / TM;
     }
-    // (classes: the whole of a shifted row)
-    if (!fp_tmap_u8_2d(&a.tx, x.p, (uint64_t)(CLASSES ? x.ld : a.K), (uint64_t)x.rows, (uint64_t)x.ld, MI_BK, mi_box_rows(BN), true))
+    const uint64_t xk = (uint64_t)(CLASSES ? x.ld : a.K);  // (classes: the whole of a shifted row)
+    if (!fp_tmap_u8_2d(&a.tx, x.p, xk, (uint64_t)x.rows, (uint64_t)x.ld, MI_BK, mi_box_rows(BN), true))
         return fp_fail(c, FP_ERR_CUDA, "fp_matmul_i8: tensor map encoding failed");
     a.per = SPLIT ? (((BN + split - 1) / split) + 7) & ~7 : 0;
     const size_t extra = (SPLIT ? (size_t)split * a.per * MI_BM * 4 : 0) + 8 * ((size_t)a.E + 1) + 1024;
     a.stages = (int)std::min<size_t>(MI_MAX_STAGES, (MI_SMEM - extra) / STAGE);
-    if (extra + 2 * STAGE > (size_t)MI_SMEM) return fp_fail(c, FP_ERR_SHAPE, "fp_matmul_i8: too many experts");  // (never: 3 stages at E = 4096)
+    if (extra + 2 * STAGE > (size_t)MI_SMEM)  // (three stages at 4096 experts)
+        return fp_fail(c, FP_ERR_SHAPE, "fp_matmul_i8: too many experts for the shared memory");
     auto kern = matmul_i8_kernel<BN, SPLIT, PAIR, CLASSES>;
     FP_CUDA(c, fp_op_smem(c, mi_kernel_bit<BN, SPLIT, PAIR, CLASSES>(), kern, MI_SMEM));
     const int64_t tiles = token_tiles * a.mt;

@@ -812,6 +812,67 @@ def test_other_stream_explicitly(env):
     assert torch.equal(s["out"], want)
 
 
+def test_two_streams_at_once(env):
+    # plain calls of one context on two streams, products of every shape among them, give what they give alone
+    torch, fp, ctx = env
+    shapes = [(1, 640, 5120, 0), (40, 300, 1024, 0), (400, 520, 512, 0), (1500, 2100, 256, 0), (3, 900, 333, 3), (90, 200, 77, 1)]
+    side = [torch.cuda.Stream() for _ in range(2)]
+    work = []
+    for i, (N, M, K, pad) in enumerate(shapes * 2):
+        w, x, ws, xs, y, yb = product_case(torch, N, M, K, 0, "bfloat16", i, padx=pad)
+        q, s = torch.empty(N, K, dtype=torch.int8, device="cuda"), torch.empty(N, device="cuda")
+        work.append((w, x, ws, xs, y, x.float(), q, s, side[i % 2]))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for w, x, ws, xs, y, xf, q, s, st in work:
+            ctx.quantize_rows(xf, q, s, stream=st)
+            ctx.matmul_i8(w, x, y, ws, xs, stream=st)
+    torch.cuda.synchronize()
+    for w, x, ws, xs, y, xf, q, s, st in work:
+        check_product(torch, w, x, ws, xs, y)
+        assert np.array_equal(q.cpu().numpy(), quantized(xf.double().cpu().numpy())[0])
+
+
+def test_the_same_row_twice(env):
+    # positions are the caller's: a row that two choices share is added twice and gets each one's gradient term
+    torch, fp, ctx = env
+    rows = torch.randn(3, 96, device="cuda")
+    pos = torch.tensor([[1, 1], [2, 0]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[0.5, 0.25], [1.0, 2.0]], device="cuda")
+    out, dw = torch.empty(2, 96, device="cuda"), torch.empty(2, 2, device="cuda")
+    ctx.moe_combine(rows, pos, out, weights=w)
+    r = rows.double().cpu().numpy()
+    within(out[0], 0.75 * r[1], 0.0, 4 * U * np.abs(r[1]))
+    ctx.moe_combine_grad(out, rows, pos, w, dweights=dw)
+    assert float(dw[0, 0]) == float(dw[0, 1])
+
+
+def test_choices_beyond_a_few(env):
+    # more choices a token than are kept at a time, and a token that chooses one expert often
+    torch, fp, ctx = env
+    rng = np.random.default_rng(8)
+    T, k, E, M = 5, 70, 6, 48
+    e = rng.integers(-1, E, (T, k)).astype(np.int32)
+    e[2] = 4
+    off, pos = sorted_choices(e, E)
+    o, p = torch.empty(E + 1, dtype=torch.int32, device="cuda"), torch.empty(T, k, dtype=torch.int32, device="cuda")
+    ctx.moe_sort(torch.from_numpy(e).cuda(), E, o, p)
+    assert np.array_equal(o.cpu().numpy(), off) and np.array_equal(p.cpu().numpy(), pos)
+    x = torch.from_numpy(rng.integers(-8, 9, (T, M)).astype(np.float32)).cuda()
+    rows, back = torch.zeros(T * k, M, device="cuda"), torch.empty(T, M, device="cuda")
+    ctx.moe_dispatch(x, p, rows)
+    ctx.moe_combine(rows, p, back)
+    assert torch.equal(back, x * torch.from_numpy((e >= 0).sum(1)).cuda()[:, None])
+    w = torch.from_numpy(rng.integers(-3, 4, (T, k)).astype(np.float32)).cuda()
+    dr, dw = torch.zeros_like(rows), torch.empty(T, k, device="cuda")
+    ctx.moe_combine_grad(x, rows, p, w, dr, dw)
+    live = torch.from_numpy(e >= 0).cuda()
+    assert torch.equal(dw, torch.where(live, (x * x).sum(1, keepdim=True), 0.0))
+    want = torch.zeros_like(rows)
+    want[p[live].long()] = (w[:, :, None] * x[:, None])[live]
+    assert torch.equal(dr, want)
+
+
 def test_repeats_give_the_same_bits(env):
     torch, fp, ctx = env
     s = layer_state(torch, 90, 3, 8, 160, 224, 9)
