@@ -50,6 +50,27 @@ class _LRec(C.Structure):
 
 _lib = None
 _raw_stream = None  # device -> its current stream's handle
+_bound = None  # the operators' compiled way into the library, or _Unbound
+
+
+class _Unbound:
+    """In place of the compiled binding where there is none: it does no call, and the methods go their own way."""
+
+    @staticmethod
+    def quantize_rows(*_):
+        return None
+
+    matmul_i8 = moe_sort = moe_dispatch = moe_combine = moe_combine_grad = quantize_rows
+
+
+def _load_binding():
+    global _bound
+    try:
+        import torch  # noqa: F401  (the libraries that it links against)
+        from . import _binding as _bound
+    except ImportError:
+        _bound = _Unbound
+    return _bound
 
 
 def lib():
@@ -1056,25 +1077,33 @@ class Context:
             raise ValueError(f"{what}: {name} must be float32, float16 or bfloat16, not {_dtype(t)}")
         return code
 
+    def _int32(self, what: str, name: str, v: int):
+        """A count that the C call takes as an int."""
+        if v > 0x7FFFFFFF:
+            raise ValueError(f"{what}: {name} must be below 2^31, not {v}")
+
     def _positions(self, what: str, pos, T: int) -> tuple:
         """(address, choices a token) of T x k int32 positions."""
         shape = pos.shape
         if len(shape) != 2:
             self._refuse(what, "pos", pos, (T, None), "int32", True)
         k = shape[1]
+        self._int32(what, "pos' choices a token", k)
         return self._dense(what, "pos", pos, (T, k), "int32"), k
 
     def quantize_rows(self, x, q, scale, pos=None, stream=None) -> None:
         """int8 rows with one scale a token: scale = max |x| / 127, q the nearest integers to x / scale.
         x: T x K float32, float16 or bfloat16; q: R x K int8; scale: R float32. pos (T x k int32, from
         moe_sort): token t goes to the rows pos[t], else to row t. Rows without a token are left."""
-        what = "quantize_rows"
-        xp, T, K, ldx = self._rows(what, "x", x, None, None, None)
-        xt = self._real(what, "x", x)
-        qp, R, _, ldq = self._rows(what, "q", q, None, K, "int8")
-        sp = self._dense(what, "scale", scale, (R,), "float32")
-        pp, k = self._positions(what, pos, T) if pos is not None else (None, 0)
-        rc = self._L.fp_quantize_rows(self.h, xp, xt, T, K, ldx, pp, k, R, qp, ldq, sp, self._op_stream(stream))
+        rc = (_bound or _load_binding()).quantize_rows(self.h, self.device, x, q, scale, pos, stream)
+        if rc is None:
+            what = "quantize_rows"
+            xp, T, K, ldx = self._rows(what, "x", x, None, None, None)
+            xt = self._real(what, "x", x)
+            qp, R, _, ldq = self._rows(what, "q", q, None, K, "int8")
+            sp = self._dense(what, "scale", scale, (R,), "float32")
+            pp, k = self._positions(what, pos, T) if pos is not None else (None, 0)
+            rc = self._L.fp_quantize_rows(self.h, xp, xt, T, K, ldx, pp, k, R, qp, ldq, sp, self._op_stream(stream))
         if rc:
             self._check(rc, "fp_quantize_rows")
 
@@ -1083,25 +1112,28 @@ class Context:
         with offsets (E + 1 int32, from moe_sort) E x M x K and E x M: expert e has the rows
         offsets[e] .. offsets[e + 1] - 1. x: N x K int8; x_scale: N float32; y: N x M float32, float16 or
         bfloat16; rows of y that no expert has are left."""
-        what = "matmul_i8"
-        if offsets is None:
-            wp, M, K, ldw = self._rows(what, "w", w, None, None, "int8")
-            E, op = 1, None
-            wsp = self._dense(what, "w_scale", w_scale, (M,), "float32")
-        else:
-            shape = w.shape
-            if len(shape) != 3:
-                raise ValueError(f"{what}: w must be experts x channels x K, not {_times(shape)}")
-            E, M, K = shape
-            ldw = K
-            wp = self._dense(what, "w", w, (E, M, K), "int8")
-            wsp = self._dense(what, "w_scale", w_scale, (E, M), "float32")
-            op = self._dense(what, "offsets", offsets, (E + 1,), "int32")
-        xp, N, _, ldx = self._rows(what, "x", x, None, K, "int8")
-        xsp = self._dense(what, "x_scale", x_scale, (N,), "float32")
-        yp, _, _, ldy = self._rows(what, "y", y, N, M, None)
-        rc = self._L.fp_matmul_i8(self.h, wp, ldw, wsp, E, M, K, xp, ldx, xsp, N, op, yp, self._real(what, "y", y), ldy,
-                                  self._op_stream(stream))
+        rc = (_bound or _load_binding()).matmul_i8(self.h, self.device, w, x, y, w_scale, x_scale, offsets, stream)
+        if rc is None:
+            what = "matmul_i8"
+            if offsets is None:
+                wp, M, K, ldw = self._rows(what, "w", w, None, None, "int8")
+                E, op = 1, None
+                wsp = self._dense(what, "w_scale", w_scale, (M,), "float32")
+            else:
+                shape = w.shape
+                if len(shape) != 3:
+                    raise ValueError(f"{what}: w must be experts x channels x K, not {_times(shape)}")
+                E, M, K = shape
+                ldw = K
+                self._int32(what, "w's experts", E)
+                wp = self._dense(what, "w", w, (E, M, K), "int8")
+                wsp = self._dense(what, "w_scale", w_scale, (E, M), "float32")
+                op = self._dense(what, "offsets", offsets, (E + 1,), "int32")
+            xp, N, _, ldx = self._rows(what, "x", x, None, K, "int8")
+            xsp = self._dense(what, "x_scale", x_scale, (N,), "float32")
+            yp, _, _, ldy = self._rows(what, "y", y, N, M, None)
+            rc = self._L.fp_matmul_i8(self.h, wp, ldw, wsp, E, M, K, xp, ldx, xsp, N, op, yp, self._real(what, "y", y),
+                                      ldy, self._op_stream(stream))
         if rc:
             self._check(rc, "fp_matmul_i8")
 
@@ -1109,12 +1141,15 @@ class Context:
         """Tokens sorted by expert. e: T x k (or T) int32, every token's experts, outside [0, E) for none;
         offsets: E + 1 int32 and pos: int32 of e's shape are written: the experts' first rows, and the row
         of every choice (by expert, then in the order of the choices; -1 for none)."""
-        what = "moe_sort"
-        shape = e.shape
-        ep = self._dense(what, "e", e, shape, "int32")
-        op = self._dense(what, "offsets", offsets, (E + 1,), "int32")
-        pp = self._dense(what, "pos", pos, shape, "int32")
-        rc = self._L.fp_moe_sort(self.h, ep, e.numel(), E, op, pp, self._op_stream(stream))
+        rc = (_bound or _load_binding()).moe_sort(self.h, self.device, e, E, offsets, pos, stream)
+        if rc is None:
+            what = "moe_sort"
+            shape = e.shape
+            ep = self._dense(what, "e", e, shape, "int32")
+            self._int32(what, "E", E)
+            op = self._dense(what, "offsets", offsets, (E + 1,), "int32")
+            pp = self._dense(what, "pos", pos, shape, "int32")
+            rc = self._L.fp_moe_sort(self.h, ep, e.numel(), E, op, pp, self._op_stream(stream))
         if rc:
             self._check(rc, "fp_moe_sort")
 
@@ -1122,13 +1157,15 @@ class Context:
         """rows[pos[t][j]] = x[t]. x: T x K of any type; pos: T x k int32; rows: R x K of x's type. The
         experts' inputs of prove_dispatch, for any k. Rows without a token are left. Its gradient is
         moe_combine without weights."""
-        what = "moe_dispatch"
-        xp, T, K, ldx = self._rows(what, "x", x, None, None, None)
-        rp, R, _, ldr = self._rows(what, "rows", rows, None, K, _dtype(x))
-        pp, k = self._positions(what, pos, T)
-        size = x.element_size()
-        rc = self._L.fp_moe_dispatch(self.h, xp, T, K * size, ldx * size, pp, k, R, rp, ldr * size,
-                                     self._op_stream(stream))
+        rc = (_bound or _load_binding()).moe_dispatch(self.h, self.device, x, pos, rows, stream)
+        if rc is None:
+            what = "moe_dispatch"
+            xp, T, K, ldx = self._rows(what, "x", x, None, None, None)
+            rp, R, _, ldr = self._rows(what, "rows", rows, None, K, _dtype(x))
+            pp, k = self._positions(what, pos, T)
+            size = x.element_size()
+            rc = self._L.fp_moe_dispatch(self.h, xp, T, K * size, ldx * size, pp, k, R, rp, ldr * size,
+                                         self._op_stream(stream))
         if rc:
             self._check(rc, "fp_moe_dispatch")
 
@@ -1136,14 +1173,16 @@ class Context:
         """out[t] = base[t] + sum_j weights[t][j] rows[pos[t][j]] (fp32 sums). rows: R x M and out: T x M
         float32, float16 or bfloat16; pos: T x k int32; weights: T x k float32 or None (ones); base: as out
         (it may be out) or None."""
-        what = "moe_combine"
-        rp, R, M, ldr = self._rows(what, "rows", rows, None, None, None)
-        op, T, _, ldo = self._rows(what, "out", out, None, M, None)
-        pp, k = self._positions(what, pos, T)
-        wp = self._dense(what, "weights", weights, (T, k), "float32") if weights is not None else None
-        bp, _, _, ldb = self._rows(what, "base", base, T, M, _dtype(out)) if base is not None else (None, 0, 0, 0)
-        rc = self._L.fp_moe_combine(self.h, rp, self._real(what, "rows", rows), R, ldr, pp, wp, bp, ldb, T, k, M, op,
-                                    self._real(what, "out", out), ldo, self._op_stream(stream))
+        rc = (_bound or _load_binding()).moe_combine(self.h, self.device, rows, pos, out, weights, base, stream)
+        if rc is None:
+            what = "moe_combine"
+            rp, R, M, ldr = self._rows(what, "rows", rows, None, None, None)
+            op, T, _, ldo = self._rows(what, "out", out, None, M, None)
+            pp, k = self._positions(what, pos, T)
+            wp = self._dense(what, "weights", weights, (T, k), "float32") if weights is not None else None
+            bp, _, _, ldb = self._rows(what, "base", base, T, M, _dtype(out)) if base is not None else (None, 0, 0, 0)
+            rc = self._L.fp_moe_combine(self.h, rp, self._real(what, "rows", rows), R, ldr, pp, wp, bp, ldb, T, k, M,
+                                        op, self._real(what, "out", out), ldo, self._op_stream(stream))
         if rc:
             self._check(rc, "fp_moe_combine")
 
@@ -1151,16 +1190,19 @@ class Context:
         """Gradients of moe_combine: drows[pos[t][j]] = weights[t][j] dout[t] (rows' type) and
         dweights[t][j] = <dout[t], rows[pos[t][j]]> (T x k float32), either of them None when it is not
         wanted. dout: T x M (base's gradient as it is). Rows of drows without a choice are left."""
-        what = "moe_combine_grad"
-        dp, T, M, ldd = self._rows(what, "dout", dout, None, None, None)
-        rp, R, _, ldr = self._rows(what, "rows", rows, None, M, None)
-        pp, k = self._positions(what, pos, T)
-        wp = self._dense(what, "weights", weights, (T, k), "float32") if weights is not None else None
-        dwp = self._dense(what, "dweights", dweights, (T, k), "float32") if dweights is not None else None
-        gp, _, _, ldg = self._rows(what, "drows", drows, R, M, _dtype(rows)) if drows is not None else (None, 0, 0, 0)
-        rc = self._L.fp_moe_combine_grad(self.h, dp, self._real(what, "dout", dout), ldd, rp,
-                                         self._real(what, "rows", rows), R, ldr, pp, wp, T, k, M, gp, ldg, dwp,
-                                         self._op_stream(stream))
+        rc = (_bound or _load_binding()).moe_combine_grad(self.h, self.device, dout, rows, pos, weights, drows,
+                                                                dweights, stream)
+        if rc is None:
+            what = "moe_combine_grad"
+            dp, T, M, ldd = self._rows(what, "dout", dout, None, None, None)
+            rp, R, _, ldr = self._rows(what, "rows", rows, None, M, None)
+            pp, k = self._positions(what, pos, T)
+            wp = self._dense(what, "weights", weights, (T, k), "float32") if weights is not None else None
+            dwp = self._dense(what, "dweights", dweights, (T, k), "float32") if dweights is not None else None
+            gp, _, _, ldg = self._rows(what, "drows", drows, R, M, _dtype(rows)) if drows is not None else (None, 0, 0, 0)
+            rc = self._L.fp_moe_combine_grad(self.h, dp, self._real(what, "dout", dout), ldd, rp,
+                                             self._real(what, "rows", rows), R, ldr, pp, wp, T, k, M, gp, ldg, dwp,
+                                             self._op_stream(stream))
         if rc:
             self._check(rc, "fp_moe_combine_grad")
 

@@ -1,10 +1,13 @@
-"""Build libfp.so in-tree with nvcc for sm_100a (cross-compiles without a GPU)."""
+"""Build libfp.so in-tree with nvcc for sm_100a (cross-compiles without a GPU), and beside it _binding.so, the
+layer operators' short way from PyTorch's tensors into it."""
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -13,6 +16,7 @@ CSRC = HERE / "csrc"
 INCLUDE = HERE.parent / "include"
 OBJ = HERE / "_build"
 LIB = HERE / "libfp.so"
+BINDING = HERE / "_binding.so"
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -54,7 +58,33 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
         cmd = [NVCC, *ARCH, "-shared", "-o", str(tmp), *map(str, objs)]
         subprocess.run(cmd, check=True, capture_output=not verbose)
         os.replace(tmp, LIB)
+    build_binding(force, verbose)
     return LIB
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> Path | None:
+    """Compile csrc/binding.cpp for this interpreter and its PyTorch; None where either lacks what that takes (the
+    operators' methods then do without it)."""
+    spec, python = importlib.util.find_spec("torch"), Path(sysconfig.get_paths()["include"])
+    root = Path(spec.origin).resolve().parent if spec and spec.origin else None
+    if root is None or not (root / "lib" / "libc10_cuda.so").exists() or not (python / "Python.h").exists():
+        return None
+    src = CSRC / "binding.cpp"
+    newest = max(p.stat().st_mtime for p in (src, INCLUDE / "fp.h", Path(__file__), root / "version.py"))
+    if not force and BINDING.exists() and BINDING.stat().st_mtime >= newest:
+        return BINDING
+    tmp = BINDING.with_suffix(f".so.{os.getpid()}")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{root / 'include'}",
+           f"-I{python}", f"-I{Path(NVCC).resolve().parents[1] / 'include'}", str(src), "-o", str(tmp),
+           f"-L{root / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-L{HERE}", "-l:libfp.so",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed:\n{r.stderr}{r.stdout}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

@@ -178,3 +178,32 @@ def test_kernels_have_names(fp):
     for n in ("quant_rows", "matmul_i8", "realign_rows", "moe_sort", "moe_dispatch", "moe_combine", "moe_grad"):
         assert n in names
     assert len(set(names)) == len(names)
+
+
+def test_binding_leaves_what_it_does_not_know(fp):
+    # the compiled binding makes no call for tensors of the CPU, stand-ins, wrong counts of arguments or what
+    # is no number, and raises nothing: the methods' checks say what is wrong
+    import torch
+    short = fp._load_binding()
+    f, i, q = torch.zeros(2, 4), torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int8)
+    s = torch.zeros(2)
+    for h in (None, 1 << 20, "h", 1 << 80):
+        for stream in (0, 1 << 80, "s", object()):
+            assert short.quantize_rows(h, 0, f, q, s, i, stream) is None
+            assert short.matmul_i8(h, 0, q, q, f, s, s, None, stream) is None
+            assert short.moe_sort(h, 0, i, 4, i, i, stream) is None
+            assert short.moe_sort(h, 0, i, 1 << 80, i, i, stream) is None
+            assert short.moe_dispatch(h, 0, f, i, f, stream) is None
+            assert short.moe_combine(h, 0, f, i, f, None, None, stream) is None
+            assert short.moe_combine_grad(h, 0, f, f, i, None, None, None, stream) is None
+    t = T(2, 4)
+    assert short.moe_combine(1 << 20, 0, t, t, t, None, None, 0) is None
+    assert short.moe_dispatch() is None and short.moe_sort(1, 2, 3) is None
+
+
+def test_counts_past_an_int(ctx):
+    big = 1 << 32
+    refused(lambda: ctx.moe_sort(T(4, 1, dtype="int32"), big + 3, T(big + 4, dtype="int32"), T(4, 1, dtype="int32"), stream=0), "E must be below")
+    refused(lambda: ctx.moe_dispatch(T(1, 8), T(1, big + 1, dtype="int32"), T(4, 8), stream=0), "pos' choices")
+    refused(lambda: ctx.matmul_i8(T(big + 1, 1, 1, dtype="int8"), T(4, 1, dtype="int8"), T(4, 1), T(big + 1, 1), T(4),
+                                  offsets=T(big + 2, dtype="int32"), stream=0), "experts must be below")

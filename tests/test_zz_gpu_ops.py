@@ -891,3 +891,124 @@ def test_another_device_than_the_current(env):
         ctx.quantize_rows(x, q, s)
         assert torch.cuda.current_device() == 1
         assert np.array_equal(q.cpu().numpy(), quantized(x.double().cpu().numpy())[0])
+
+
+# ---- the two ways of a call: the compiled binding, and the methods' own checks and conversions -----------
+
+def unbound(fp, monkeypatch):
+    monkeypatch.setattr(fp, "_bound", fp._Unbound)
+
+
+@pytest.mark.parametrize("T,k,E,d,F", [(1, 2, 4, 64, 96), (33, 3, 8, 100, 77)])
+def test_both_ways_give_the_same(env, monkeypatch, T, k, E, d, F):
+    torch, fp, ctx = env
+
+    def run():
+        s = layer_state(torch, T, k, E, d, F, 3 * T)
+        layer(torch, ctx, s)
+        s["x_rows"] = torch.zeros(T * k, d, dtype=torch.bfloat16, device="cuda")
+        ctx.moe_dispatch(s["x"], s["pos"], s["x_rows"])
+        s["dz"], s["dw"] = torch.zeros_like(s["z"]), torch.empty_like(s["weights"])
+        ctx.moe_combine_grad(s["out"], s["z"], s["pos"], s["weights"], s["dz"], s["dw"])
+        s["dense"] = torch.zeros(T * k, d, device="cuda")
+        ctx.matmul_i8(s["w2"][0], s["aq"], s["dense"], s["w2s"][0], s["as"])
+        return s
+
+    one = run()
+    unbound(fp, monkeypatch)
+    other = run()
+    for name in one:
+        assert name == "E" or torch.equal(one[name], other[name]), name
+
+
+def test_plain_calls_go_through_the_binding(env, monkeypatch):
+    torch, fp, ctx = env
+    short = fp._load_binding()
+    if short is fp._Unbound:
+        pytest.skip("built without the compiled binding")
+    seen = []
+
+    class Watch:
+        def __getattr__(self, name):
+            def call(*a):
+                rc = getattr(short, name)(*a)
+                seen.append((name, rc))
+                return rc
+            return call
+
+    monkeypatch.setattr(fp, "_bound", Watch())
+    T, K, M, k, E = 5, 40, 24, 2, 4
+    x = torch.randn(T, K, device="cuda")
+    wide_q = torch.zeros(T * k, K + 8, dtype=torch.int8, device="cuda")
+    q, sc = wide_q[:, :K], torch.zeros(T * k, device="cuda")
+    e = torch.arange(T * k, dtype=torch.int32, device="cuda").view(T, k) % E
+    off, pos = torch.zeros(E + 1, dtype=torch.int32, device="cuda"), torch.zeros_like(e)
+    w = torch.ones(E, M, K, dtype=torch.int8, device="cuda")
+    ws, y = torch.ones(E, M, device="cuda"), torch.zeros(T * k, M, device="cuda").half()
+    out, dw, rows = torch.zeros(T, M, device="cuda"), torch.zeros(T, k, device="cuda"), torch.zeros(T * k, M, device="cuda")
+    st = torch.cuda.current_stream()
+    for stream in (None, st, st.cuda_stream):
+        ctx.moe_sort(e, E, off, pos, stream=stream)
+        ctx.quantize_rows(x, q, sc, pos=pos, stream=stream)
+        ctx.matmul_i8(w, q, y, ws, sc, offsets=off, stream=stream)
+        ctx.matmul_i8(w[1], q, y, ws[1], sc, stream=stream)
+        ctx.moe_dispatch(out, pos, rows, stream=stream)
+        ctx.moe_combine(y, pos, out, stream=stream)
+        ctx.moe_combine_grad(out, y, pos, dweights=dw, stream=stream)
+    torch.cuda.synchronize()
+    assert len(seen) == 21 and all(rc == 0 for _, rc in seen), seen
+
+    class Sub(torch.Tensor):
+        pass
+
+    del seen[:]  # what the binding does not know goes the methods' own way
+    ctx.moe_combine(y, pos, out.as_subclass(Sub))
+    assert seen == [("moe_combine", None)]
+
+
+@pytest.mark.parametrize("way", ["binding", "methods"])
+def test_refusals_of_device_tensors(env, monkeypatch, way):
+    torch, fp, ctx = env
+    if way == "methods":
+        unbound(fp, monkeypatch)
+    T, K, M, k, E = 4, 32, 16, 2, 4
+    x, q, sc = torch.ones(T, K, device="cuda"), torch.zeros(T, K, dtype=torch.int8, device="cuda"), torch.ones(T, device="cuda")
+    w, ws, y = torch.zeros(M, K, dtype=torch.int8, device="cuda"), torch.ones(M, device="cuda"), torch.zeros(T, M, device="cuda")
+    e = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    off, pos = torch.zeros(E + 1, dtype=torch.int32, device="cuda"), torch.zeros_like(e)
+    rows, wt = torch.zeros(T * k, K, device="cuda"), torch.ones(T, k, device="cuda")
+    cases = [
+        (lambda: ctx.quantize_rows(x.double(), q, sc), "x must be float32"),
+        (lambda: ctx.quantize_rows(x.cpu(), q, sc), "x must be on cuda:0"),
+        (lambda: ctx.quantize_rows(x, q[:, 1:], sc), "q must be"),
+        (lambda: ctx.quantize_rows(x, q, sc[1:]), "scale must be"),
+        (lambda: ctx.quantize_rows(x, q, sc.double()), "scale must be float32"),
+        (lambda: ctx.quantize_rows(x.t(), q, sc), "rows must be contiguous"),
+        (lambda: ctx.quantize_rows(x, q, sc, pos=pos[1:]), "pos must be"),
+        (lambda: ctx.quantize_rows(x, q, sc, pos=pos.long()), "pos must be int32"),
+        (lambda: ctx.matmul_i8(w, q[:, :8], y, ws, sc), "x must be"),
+        (lambda: ctx.matmul_i8(w, q, y[:, :8], ws, sc), "y must be"),
+        (lambda: ctx.matmul_i8(w, q, y.int(), ws, sc), "y must be float32"),
+        (lambda: ctx.matmul_i8(w, q, y, ws[1:], sc), "w_scale must be"),
+        (lambda: ctx.matmul_i8(w, q, y, ws, sc[1:]), "x_scale must be"),
+        (lambda: ctx.matmul_i8(w[None], q, y, ws[None], sc, offsets=off), "offsets must be"),
+        (lambda: ctx.matmul_i8(w, q, y, ws, sc, offsets=off), "w must be"),
+        (lambda: ctx.moe_sort(e, E + 1, off, pos), "offsets must be"),
+        (lambda: ctx.moe_sort(e.t(), E, off, pos.t()), "e must be contiguous"),
+        (lambda: ctx.moe_sort(e, E, off, pos[1:]), "pos must be"),
+        (lambda: ctx.moe_dispatch(x, pos, rows.half()), "rows must be float32"),
+        (lambda: ctx.moe_dispatch(x, pos[1:], rows), "pos must be"),
+        (lambda: ctx.moe_combine(rows, pos, x[:, 1:]), "out must be"),
+        (lambda: ctx.moe_combine(rows, pos, x, weights=wt.half()), "weights must be float32"),
+        (lambda: ctx.moe_combine(rows, pos, x, base=x.half()), "base must be float32"),
+        (lambda: ctx.moe_combine_grad(x, rows[:, 1:], pos), "rows must be"),
+        (lambda: ctx.moe_combine_grad(x, rows, pos, wt, drows=rows[1:]), "drows must be"),
+        (lambda: ctx.moe_combine_grad(x, rows, pos, wt, dweights=wt[:, :1]), "dweights must be"),
+    ]
+    for call, text in cases:
+        with pytest.raises(ValueError, match=text):
+            call()
+    # the C call's own errors come through both ways
+    with pytest.raises(fp.FpError, match="fp_moe_sort") as err:
+        ctx.moe_sort(e, 5000, torch.zeros(5001, dtype=torch.int32, device="cuda"), pos)
+    assert err.value.code == -2
