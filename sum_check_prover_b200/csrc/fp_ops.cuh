@@ -105,19 +105,23 @@ __device__ __forceinline__ FpSpan fp_span(const T* p, int64_t rows, int64_t ld, 
     return FpSpan{reinterpret_cast<const char*>(p), reinterpret_cast<const char*>(p + (rows - 1) * ld + cols)};
 }
 
-// 16 bytes from any address: the two aligned 16 bytes that they lie in, shifted. False where those are not
-// both inside the span (the matrix's ends).
-__device__ __forceinline__ bool fp_load16_any(const void* p, const FpSpan& span, uint32_t (&o)[4]) {
-    const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
-    const char* q = reinterpret_cast<const char*>(p) - sh;
-    if (q < span.lo || q + 32 > span.hi) return false;
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(q)), b = __ldg(reinterpret_cast<const uint4*>(q) + 1);
+// the 16 bytes from byte `sh` of a and b, one after the other
+__device__ __forceinline__ void fp_shift16(const uint4& a, const uint4& b, uint32_t sh, uint32_t* o) {
     uint32_t w[7] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
     if (sh & 8) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = b.w;
     if (sh & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
     const uint32_t bits = 8 * (sh & 3);
 #pragma unroll
     for (int i = 0; i < 4; i++) o[i] = __funnelshift_r(w[i], w[i + 1], bits);
+}
+
+// 16 bytes from any address: the two aligned 16 bytes that they lie in, shifted. False where those are not
+// both inside the span (the matrix's ends).
+__device__ __forceinline__ bool fp_load16_any(const void* p, const FpSpan& span, uint32_t (&o)[4]) {
+    const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    const char* q = reinterpret_cast<const char*>(p) - sh;
+    if (q < span.lo || q + 32 > span.hi) return false;
+    fp_shift16(__ldg(reinterpret_cast<const uint4*>(q)), __ldg(reinterpret_cast<const uint4*>(q) + 1), sh, o);
     return true;
 }
 
@@ -144,20 +148,9 @@ struct FpWords {
             w[0] = *reinterpret_cast<const uint8_t*>(p);
         }
     }
-    // from any address that is a multiple of UNIT
+    // from a multiple of UNIT, UNIT bytes at a time
     template <int UNIT>
-    __device__ __forceinline__ void load_any(const void* p, const FpSpan& span) {
-        if constexpr (BYTES % 16 == 0) {
-            bool ok = true;
-#pragma unroll
-            for (int i = 0; i < BYTES / 16; i++) {
-                uint32_t o[4] = {0, 0, 0, 0};
-                ok = ok && fp_load16_any(reinterpret_cast<const char*>(p) + 16 * i, span, o);
-#pragma unroll
-                for (int j = 0; j < 4; j++) w[4 * i + j] = o[j];
-            }
-            if (ok) return;
-        }
+    __device__ __forceinline__ void load_units(const void* p) {
         if constexpr (UNIT == 4) {
 #pragma unroll
             for (int i = 0; i < W; i++) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
@@ -191,17 +184,9 @@ struct FpWords {
     }
 };
 
-// V consecutive real values
+// V consecutive values
 template <typename T, int V>
 struct FpVec : FpWords<V * (int)sizeof(T)> {
-    // ANY: from any multiple of the element's size
-    template <bool ANY>
-    __device__ __forceinline__ void load_row(const T* p, const FpSpan& span) {
-        if constexpr (ANY)
-            this->template load_any<(int)sizeof(T)>(p, span);
-        else
-            this->load(p);
-    }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(T) == 4) {
             return __uint_as_float(this->w[i]);
@@ -230,5 +215,54 @@ struct FpVec : FpWords<V * (int)sizeof(T)> {
                 }
             }
         }
+    }
+};
+
+// A row's vectors of V values. ANY: the row begins at any multiple of its element's size, and each 16 bytes are the
+// two aligned 16 bytes that they lie in, shifted; `load` is false for a vector whose aligned bytes are not all inside
+// the matrix (its first and last ones), which `slow` then reads. `load` has no branches, so that a thread's loads do not
+// wait for one another.
+template <typename T, int V, bool ANY>
+struct FpRow {
+    static constexpr int BYTES = V * (int)sizeof(T);
+    static constexpr bool SHIFT = ANY && BYTES % 16 == 0;
+    const T* p;
+    const char* q;
+    uint32_t sh;
+    int first, end;
+    __device__ __forceinline__ FpRow() {}
+    __device__ __forceinline__ FpRow(const T* row, const FpSpan& span) : p(row) {
+        if constexpr (SHIFT) {
+            sh = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15);
+            q = reinterpret_cast<const char*>(row) - sh;
+            first = q < span.lo;
+            end = (int)min((int64_t)0x7fffffff, (int64_t)(span.hi - q - 16) / BYTES);
+        }
+    }
+    __device__ __forceinline__ bool load(FpVec<T, V>& v, int c) const {
+        if constexpr (SHIFT) {
+            const bool ok = c >= first && c < end;
+            const uint4* at = reinterpret_cast<const uint4*>(q + (int64_t)c * BYTES);
+            uint4 b[BYTES / 16 + 1];
+#pragma unroll
+            for (int i = 0; i <= BYTES / 16; i++) b[i] = ok ? __ldg(at + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < BYTES / 16; i++) fp_shift16(b[i], b[i + 1], sh, &v.w[4 * i]);
+            return ok;
+        } else if constexpr (ANY) {
+            slow(v, c);
+            return true;
+        } else {
+            v.load(p + (int64_t)c * V);
+            return true;
+        }
+    }
+    __device__ __forceinline__ void slow(FpVec<T, V>& v, int c) const {
+        v.template load_units<(int)sizeof(T)>(p + (int64_t)c * V);
+    }
+    __device__ __forceinline__ FpVec<T, V> get(int c) const {
+        FpVec<T, V> v;
+        if (!load(v, c)) slow(v, c);
+        return v;
     }
 };

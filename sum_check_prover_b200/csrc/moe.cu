@@ -155,26 +155,20 @@ constexpr int MO_CHOICES = 4;  // positions (and weights) of a token kept in reg
 // A token's row is read once and written k times, so nothing but the positions is read twice.
 //
 // rows[pos[t][j]] = x[t] in units of A bytes; one token per tpr threads, blockIdx.y a share of the columns. U
-// loads of a thread are in flight before its stores. ANY: x from any address.
-template <int A, int U, bool ANY>
+// loads of a thread are in flight before its stores.
+template <int A, int U>
 __global__ void __launch_bounds__(FP_ROW_THREADS)
     moe_dispatch_kernel(const char* __restrict__ x, int64_t T, int nvec, int64_t ldx, const int32_t* __restrict__ pos,
                         int k, int64_t R, char* __restrict__ rows, int64_t ldr, int tpr) {
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
     const char* src = x + t * ldx;
-    const FpSpan span = fp_span(x, T, ldx, (int64_t)nvec * A);
     const int step = tpr * gridDim.y;
     for (int c = threadIdx.x % tpr + tpr * blockIdx.y; c < nvec; c += U * step) {
         FpWords<A> v[U];
 #pragma unroll
         for (int u = 0; u < U; u++)
-            if (c + u * step < nvec) {
-                if constexpr (ANY)
-                    v[u].template load_any<1>(src + (int64_t)(c + u * step) * A, span);
-                else
-                    v[u].load(src + (int64_t)(c + u * step) * A);
-            }
+            if (c + u * step < nvec) v[u].load(src + (int64_t)(c + u * step) * A);
         for (int j0 = 0; j0 < k; j0 += MO_CHOICES) {
             char* dst[MO_CHOICES];
 #pragma unroll
@@ -193,13 +187,54 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
     }
 }
 
-template <int A, bool ANY>
+// The same for rows of any bytes and pitch: 16 bytes at a time from the first multiple of 16 in each destination's
+// row, x shifted to it (and read for every choice, from L1 after the first), the bytes before and behind one by one.
+// blockIdx.z: a share of the choices. 8192 rows of 5121 bf16 to two rows each, 252 MB, take 48 us, 5.2 TB/s.
+__global__ void __launch_bounds__(FP_ROW_THREADS)
+    moe_dispatch_any_kernel(const uint8_t* __restrict__ x, int64_t T, int64_t bytes, int64_t ldx, const int32_t* __restrict__ pos,
+                            int k, int64_t R, uint8_t* __restrict__ rows, int64_t ldr, int tpr) {
+    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    if (t >= T) return;
+    const uint8_t* src = x + t * ldx;
+    const FpSpan span = fp_span(x, T, ldx, bytes);
+    const int step = tpr * gridDim.y, at = threadIdx.x % tpr;
+    for (int j = blockIdx.z; j < k; j += gridDim.z) {
+        const int64_t p = __ldg(pos + t * k + j);
+        if (p < 0 || p >= R) continue;
+        uint8_t* dst = rows + p * ldr;
+        const int head = (int)min((int64_t)(-reinterpret_cast<uintptr_t>(dst) & 15), bytes), nvec = (int)((bytes - head) / 16);
+        if (blockIdx.y == 0) {
+            const int tail = (int)(bytes - head) & 15;
+            if (at < head) dst[at] = src[at];
+            if (at < tail) dst[bytes - tail + at] = src[bytes - tail + at];
+        }
+        const FpRow<uint8_t, 16, true> from(src + head, span);
+        constexpr int U = 1;  // (2: 53 us)
+        for (int c = at + tpr * blockIdx.y; c < nvec; c += U * step) {
+            FpVec<uint8_t, 16> v[U];
+            bool ok = true;
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if (c + u * step < nvec) ok &= from.load(v[u], c + u * step);
+            if (!ok) {
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    if (c + u * step < nvec) from.slow(v[u], c + u * step);
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if (c + u * step < nvec) v[u].store(dst + head + (int64_t)(c + u * step) * 16);
+        }
+    }
+}
+
+template <int A>
 void launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, int64_t ldx, const int32_t* pos, int k,
                      int64_t R, void* rows, int64_t ldr, cudaStream_t st) {
     const int nvec = (int)(bytes / A);
     constexpr int U = A == 16 ? 2 : 4;
     const FpRowGrid g = fp_row_grid(c, T, nvec, U, true);
-    moe_dispatch_kernel<A, U, ANY><<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const char*)x, T, nvec, ldx, pos, k, R,
+    moe_dispatch_kernel<A, U><<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const char*)x, T, nvec, ldx, pos, k, R,
                                                                         (char*)rows, ldr, g.tpr);
 }
 
@@ -208,9 +243,9 @@ void launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, i
 // Bound by HBM: 8192 x 5120 bf16, k = 2, 252 MB, takes 43.3 us, 5.8 TB/s (k = 1: 35 us, 4.8: a block waits for its
 // position before its one load a thread); fp32 rows of the odd width 4099, k = 2, 403 MB, 74 us, 5.4 TB/s.
 //
-// out[t] = base[t] + sum_j w[t][j] rows[pos[t][j]] in fp32, rounded once; V elements per load (ANY: from any
-// address), U vectors of a thread at a time
-template <typename RT, typename OT, int V, int U, bool ANY>
+// out[t] = base[t] + sum_j w[t][j] rows[pos[t][j]] in fp32, rounded once; V elements per load, U vectors
+// of a thread at a time
+template <typename RT, typename OT, int V, int U>
 __global__ void __launch_bounds__(FP_ROW_THREADS)
     moe_combine_kernel(const RT* __restrict__ rows, int64_t R, int64_t ldr, const int32_t* __restrict__ pos,
                        const float* __restrict__ w, const OT* base, int64_t ldb, int64_t T, int k, int nvec, OT* out,
@@ -218,14 +253,13 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
     const int step = tpr * gridDim.y;
-    const FpSpan span = fp_span(rows, R, ldr, (int64_t)nvec * V);
     for (int c = threadIdx.x % tpr + tpr * blockIdx.y; c < nvec; c += U * step) {
         float acc[U][V];
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const bool in = base && c + u * step < nvec;
             FpVec<OT, V> b;
-            if (in) b.template load_row<ANY>(base + t * ldb + (int64_t)(c + u * step) * V, fp_span(base, T, ldb, (int64_t)nvec * V));
+            if (in) b.load(base + t * ldb + (int64_t)(c + u * step) * V);
 #pragma unroll
             for (int i = 0; i < V; i++) acc[u][i] = in ? b.get(i) : 0.0f;
         }
@@ -244,7 +278,7 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
             for (int j = 0; j < 2; j++)
 #pragma unroll
                 for (int u = 0; u < U; u++)
-                    if (src[j] && c + u * step < nvec) v[j][u].template load_row<ANY>(src[j] + (int64_t)(c + u * step) * V, span);
+                    if (src[j] && c + u * step < nvec) v[j][u].load(src[j] + (int64_t)(c + u * step) * V);
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 if (!src[j]) continue;
@@ -264,6 +298,67 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
     }
 }
 
+// The same for rows of 16 bits and any width, address and pitch: V elements at a time from the first multiple of 16 bytes
+// in each output row, the rows and base shifted to it; the elements before and behind them one by one.
+template <typename RT, typename OT, int V>
+__global__ void __launch_bounds__(FP_ROW_THREADS)
+    moe_combine_odd_kernel(const RT* __restrict__ rows, int64_t R, int64_t ldr, const int32_t* __restrict__ pos,
+                           const float* __restrict__ w, const OT* base, int64_t ldb, int64_t T, int k, int M, OT* out,
+                           int64_t ldo, int tpr) {
+    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    if (t >= T) return;
+    const int step = tpr * gridDim.y, at = threadIdx.x % tpr;
+    OT* o = out + t * ldo;
+    const int head = min((int)((-reinterpret_cast<uintptr_t>(o) & 15) / sizeof(OT)), M), nvec = (M - head) / V;
+    const FpSpan span = fp_span(rows, R, ldr, M);
+    const int rest = M - nvec * V;  // head and tail
+    if (blockIdx.y == 0 && at < rest) {
+        const int c = at < head ? at : M - rest + at;
+        float acc = base ? fp_to_f(base[t * ldb + c]) : 0.0f;
+        for (int j = 0; j < k; j++) {
+            const int64_t p = __ldg(pos + t * k + j);
+            if (p >= 0 && p < R) acc = fmaf(w ? __ldg(w + t * k + j) : 1.0f, fp_to_f(rows[p * ldr + c]), acc);
+        }
+        o[c] = fp_from_f<OT>(acc);
+    }
+    for (int c = at + tpr * blockIdx.y; c < nvec; c += step) {
+        float acc[V];
+        FpVec<OT, V> b;
+        if (base) b = FpRow<OT, V, true>(base + t * ldb + head, fp_span(base, T, ldb, M)).get(c);
+#pragma unroll
+        for (int i = 0; i < V; i++) acc[i] = base ? b.get(i) : 0.0f;
+        // the loads of two choices at a time, then their sums in the order of the choices
+        for (int j0 = 0; j0 < k; j0 += 2) {
+            bool has[2], ok = true;
+            FpRow<RT, V, true> src[2];
+            FpVec<RT, V> v[2];
+            float s[2];
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int64_t p = j0 + j < k ? __ldg(pos + t * k + j0 + j) : -1;
+                has[j] = p >= 0 && p < R;
+                src[j] = FpRow<RT, V, true>(rows + (has[j] ? p : 0) * ldr + head, span);
+                s[j] = w && j0 + j < k ? __ldg(w + t * k + j0 + j) : 1.0f;
+                if (has[j]) ok &= src[j].load(v[j], c);
+            }
+            if (!ok) {
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+                    if (has[j]) src[j].slow(v[j], c);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                if (!has[j]) continue;
+#pragma unroll
+                for (int i = 0; i < V; i++) acc[i] = fmaf(s[j], v[j].get(i), acc[i]);
+            }
+        }
+        FpVec<OT, V> r;
+        r.set(acc);
+        r.store(o + head + (int64_t)c * V);
+    }
+}
+
 // ---- gradients of combine -------------------------------------------------------------------
 
 constexpr int MO_GRAD_THREADS = 512;
@@ -272,7 +367,7 @@ constexpr int MO_GRAD_THREADS = 512;
 //
 // One token per tpr threads: its k rows' gradients and the k inner products (fp32, a fixed order: a
 // thread's columns, its warp's tree, then the warps). Two choices at a time read dout once; blockIdx.y a
-// share of the choices. ANY: loads from any address.
+// share of the choices.
 template <typename RT, typename OT, int V, int U, bool ANY>
 __global__ void __launch_bounds__(MO_GRAD_THREADS)
     moe_grad_kernel(const OT* __restrict__ dout, int64_t ldd, const RT* __restrict__ rows, int64_t R, int64_t ldr,
@@ -282,8 +377,8 @@ __global__ void __launch_bounds__(MO_GRAD_THREADS)
     const int sub = threadIdx.x / tpr, tt = threadIdx.x % tpr, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + sub;
     const bool live = t < T;
-    const OT* g = dout + (live ? t : 0) * ldd;
-    const FpSpan gspan = fp_span(dout, T, ldd, (int64_t)nvec * V), rspan = fp_span(rows, R, ldr, (int64_t)nvec * V);
+    const FpRow<OT, V, ANY> g(dout + (live ? t : 0) * ldd, fp_span(dout, T, ldd, (int64_t)nvec * V));
+    const FpSpan rspan = fp_span(rows, R, ldr, (int64_t)nvec * V);
     for (int j0 = 2 * blockIdx.y; j0 < k; j0 += 2 * gridDim.y) {
         int64_t p[2];
         float s[2], dot[2] = {0.0f, 0.0f};
@@ -298,14 +393,13 @@ __global__ void __launch_bounds__(MO_GRAD_THREADS)
             FpVec<RT, V> v[2][U];
 #pragma unroll
             for (int u = 0; u < U; u++)
-                if (c + u * tpr < nvec) gv[u].template load_row<ANY>(g + (int64_t)(c + u * tpr) * V, gspan);
+                if (c + u * tpr < nvec) gv[u] = g.get(c + u * tpr);
             if (dw) {
 #pragma unroll
                 for (int j = 0; j < 2; j++)
 #pragma unroll
                     for (int u = 0; u < U; u++)
-                        if (p[j] >= 0 && c + u * tpr < nvec)
-                            v[j][u].template load_row<ANY>(rows + p[j] * ldr + (int64_t)(c + u * tpr) * V, rspan);
+                        if (p[j] >= 0 && c + u * tpr < nvec) v[j][u] = FpRow<RT, V, ANY>(rows + p[j] * ldr, rspan).get(c + u * tpr);
             }
 #pragma unroll
             for (int j = 0; j < 2; j++) {
@@ -324,7 +418,7 @@ __global__ void __launch_bounds__(MO_GRAD_THREADS)
                         FpVec<RT, V> o;
                         o.set(f);
                         RT* d = drows + p[j] * lddr + (int64_t)(c + u * tpr) * V;
-                        if (dvec) {
+                        if (!ANY || dvec) {
                             o.store(d);
                         } else {
 #pragma unroll
@@ -351,6 +445,77 @@ __global__ void __launch_bounds__(MO_GRAD_THREADS)
             }
             // 0 where there is no row: nothing was added
             if (live && tt < 2 && j0 + tt < k) dw[t * k + j0 + tt] = sum;
+        }
+    }
+}
+
+// The same for any width, address and pitch, a choice at a time: the inner product in the order of the kernel above, both
+// rows shifted to their first values, then the gradient's row from dout once more (from L1), V elements at a time from the
+// row's first multiple of 16 bytes.
+template <typename RT, typename OT, int V>
+__global__ void __launch_bounds__(MO_GRAD_THREADS)
+    moe_grad_odd_kernel(const OT* __restrict__ dout, int64_t ldd, const RT* __restrict__ rows, int64_t R, int64_t ldr,
+                        const int32_t* __restrict__ pos, const float* __restrict__ w, int64_t T, int k, int M,
+                        RT* __restrict__ drows, int64_t lddr, float* __restrict__ dw, int tpr) {
+    __shared__ float red[32];
+    const int sub = threadIdx.x / tpr, tt = threadIdx.x % tpr, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + sub;
+    const bool live = t < T;
+    const OT* g = dout + (live ? t : 0) * ldd;
+    const FpSpan gspan = fp_span(dout, T, ldd, M), rspan = fp_span(rows, R, ldr, M);
+    for (int j = blockIdx.y; j < k; j += gridDim.y) {
+        const int64_t p = live ? __ldg(pos + t * k + j) : -1;
+        const bool has = p >= 0 && p < R;
+        if (dw) {
+            float dot = 0.0f;
+            if (has) {
+                const RT* r = rows + p * ldr;
+                const FpRow<OT, V, true> gv(g, gspan);
+                const FpRow<RT, V, true> rv(r, rspan);
+                const int nvec = M / V, rest = M % V;
+                for (int c = tt; c < nvec; c += tpr) {
+                    FpVec<OT, V> x;
+                    FpVec<RT, V> y;
+                    const bool gok = gv.load(x, c), rok = rv.load(y, c);
+                    if (!gok) gv.slow(x, c);
+                    if (!rok) rv.slow(y, c);
+#pragma unroll
+                    for (int i = 0; i < V; i++) dot = fmaf(x.get(i), y.get(i), dot);
+                }
+                if (tt < rest) dot = fmaf(fp_to_f(g[nvec * V + tt]), fp_to_f(r[nvec * V + tt]), dot);
+            }
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+            if (tpr > 32) {
+                if (j > (int)blockIdx.y) __syncthreads();  // red may still be read for the choice before
+                if (lane == 0) red[warp] = dot;
+                __syncthreads();
+                if (tt == 0) {
+                    dot = 0.0f;
+                    for (int i = 0; i < tpr >> 5; i++) dot += red[sub * (tpr >> 5) + i];
+                }
+            }
+            if (live && tt == 0) dw[t * k + j] = dot;
+        }
+        if (drows && has) {
+            const float s = w ? __ldg(w + t * k + j) : 1.0f;
+            RT* d = drows + p * lddr;
+            const int head = min((int)((-reinterpret_cast<uintptr_t>(d) & 15) / sizeof(RT)), M), nvec = (M - head) / V;
+            const int rest = M - nvec * V;  // head and tail
+            if (tt < rest) {
+                const int c = tt < head ? tt : M - rest + tt;
+                d[c] = fp_from_f<RT>(s * fp_to_f(g[c]));
+            }
+            const FpRow<OT, V, true> gv(g + head, gspan);
+            for (int c = tt; c < nvec; c += tpr) {
+                const FpVec<OT, V> x = gv.get(c);
+                float f[V];
+#pragma unroll
+                for (int i = 0; i < V; i++) f[i] = s * x.get(i);
+                FpVec<RT, V> o;
+                o.set(f);
+                o.store(d + head + (int64_t)c * V);
+            }
         }
     }
 }
@@ -438,18 +603,24 @@ int fp_moe_dispatch(fp_ctx* c, const void* x, int64_t T, int64_t row_bytes, int6
                                     (uint64_t)row_bytes});
     int slot;
     fp_op_tic(c, st, K_MOE_DISPATCH, (double)row_bytes * (T + T * (double)k) + 4.0 * T * k, &slot);
-    if (al >= 16)
-        launch_dispatch<16, false>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
-    else if (fp_common_align({(uint64_t)(uintptr_t)rows, (uint64_t)ldr, (uint64_t)row_bytes}) >= 16)
-        launch_dispatch<16, true>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+    // Units of 1, 2 or 4 bytes against 16 shifted ones, us: 8192 rows of 5121 bytes 65.5 and 20.0, 20000 x 2 of 1030 24.6
+    // and 22.5; 8192 x 2 of 10242 66.3 and 48.4, 4787 x 3 of 1344 10.0 and 10.6; 8192 x 2 of 16396 89.7 and 80.6, 20000 x
+    // 2 of 1028 16.9 and 22.2; few rows: 8 of 10242 2.2 and 2.5. (Units of 8: 865 x 5 of 20664 24.4 and 30.9.)
+    if (al <= 4 && row_bytes >= 1024 * al && T * k * row_bytes >= (1 << 21)) {
+        const FpRowGrid g = fp_row_grid(c, T, row_bytes / 16, 1, true);
+        const int64_t gz = std::max<int64_t>(1, std::min<int64_t>(k, 4 * (int64_t)c->num_sms / ((int64_t)g.gx * g.gy)));
+        moe_dispatch_any_kernel<<<dim3(g.gx, g.gy, (unsigned)gz), g.threads(), 0, st>>>(
+            (const uint8_t*)x, T, row_bytes, ldx, pos, k, R, (uint8_t*)rows, ldr, g.tpr);
+    } else if (al >= 16)
+        launch_dispatch<16>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 8)
-        launch_dispatch<8, false>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<8>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 4)
-        launch_dispatch<4, false>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<4>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 2)
-        launch_dispatch<2, false>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<2>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else
-        launch_dispatch<1, false>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launch_dispatch<1>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     fp_toc(c, st, slot);
     FP_CUDA(c, cudaGetLastError());
     return FP_OK;
@@ -484,25 +655,27 @@ int fp_moe_combine(fp_ctx* c, const void* rows, int rows_type, int64_t R, int64_
         by_type(out_type, [&](auto* op) {
             using OT = std::remove_pointer_t<decltype(op)>;
             constexpr int V = 16 / sizeof(RT), OA = V * sizeof(OT) < 16 ? V * sizeof(OT) : 16;
-            const bool aligned = fp_common_align({(uint64_t)(uintptr_t)rows, (uint64_t)ldr * rs}) == 16 &&
-                                 fp_common_align({(uint64_t)(uintptr_t)base, (uint64_t)ldb * os}) >= OA;
-            // fp32 rows at odd addresses: single values (7281 x 712, k = 4: 25.6 us, and 33.9 shifted)
-            const bool vec = M % V == 0 && fp_common_align({(uint64_t)(uintptr_t)out, (uint64_t)ldo * os}) >= OA &&
-                             (aligned || rs == 2);
-            const int nvec = (int)(vec ? M / V : M);
-            auto run = [&](auto kern, int loads) {
+            const bool vec = M % V == 0 && fp_common_align({(uint64_t)(uintptr_t)rows, (uint64_t)ldr * rs}) == 16 &&
+                             fp_common_align({(uint64_t)(uintptr_t)base, (uint64_t)ldb * os, (uint64_t)(uintptr_t)out,
+                                              (uint64_t)ldo * os}) >= OA;
+            // single values against shifted vectors, us, k = 2: 8192 x 4099 bf16 72.1 and 60.5, 20000 x 1201 62.0 and 61.0, 300
+            // x 1201 3.5 and 3.9 (fp32: 73.8 and 83.3 at 8192 x 4099)
+            const bool odd = !vec && rs == 2 && M >= 2048 && T * M >= 1 << 20;
+            const int nvec = (int)(vec || odd ? M / V : M);
+            auto run = [&](auto kern, int loads, int width) {
                 const FpRowGrid g = fp_row_grid(c, T, nvec, loads, true);
                 kern<<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const RT*)rows, R, ldr, pos, weights, (const OT*)base, ldb, T,
-                                                               k, nvec, (OT*)out, ldo, g.tpr);
+                                                               k, width, (OT*)out, ldo, g.tpr);
             };
+            if constexpr (sizeof(RT) == 2) {
+                if (odd) return run(moe_combine_odd_kernel<RT, OT, V>, 1, (int)M);
+            }
             if (!vec)
-                run(moe_combine_kernel<RT, OT, 1, 4, false>, 4);
-            else if (!aligned)
-                run(moe_combine_kernel<RT, OT, V, 1, true>, 1);
+                run(moe_combine_kernel<RT, OT, 1, 4>, 4, nvec);
             else if (k <= 2)  // (8192 x 5120, k = 2: 43.2 and 43.9 us with one vector and two; 1024, k = 8: 22.9 and 19.5)
-                run(moe_combine_kernel<RT, OT, V, 1, false>, 1);
+                run(moe_combine_kernel<RT, OT, V, 1>, 1, nvec);
             else
-                run(moe_combine_kernel<RT, OT, V, 2, false>, 2);
+                run(moe_combine_kernel<RT, OT, V, 2>, 2, nvec);
         });
     });
     fp_toc(c, st, slot);
@@ -543,23 +716,39 @@ int fp_moe_combine_grad(fp_ctx* c, const void* dout, int out_type, int64_t ldd, 
         by_type(out_type, [&](auto* op) {
             using OT = std::remove_pointer_t<decltype(op)>;
             constexpr int V = 16 / sizeof(RT), OA = V * sizeof(OT) < 16 ? V * sizeof(OT) : 16;
-            // (by M alone, so that dweights' order of summation does not hang on what else is asked for)
-            const bool vec = M % V == 0, dvec = fp_common_align({(uint64_t)(uintptr_t)drows, (uint64_t)lddr * rs}) == 16;
-            const bool aligned = fp_common_align({(uint64_t)(uintptr_t)rd, (uint64_t)ldr * rs}) == 16 &&
+            // (dweights' order of summation hangs on the sizes: not on what else is asked for, nor on addresses)
+            const bool whole = M % V == 0, dvec = fp_common_align({(uint64_t)(uintptr_t)drows, (uint64_t)lddr * rs}) == 16;
+            const bool aligned = dvec && fp_common_align({(uint64_t)(uintptr_t)rd, (uint64_t)ldr * rs}) == 16 &&
                                  fp_common_align({(uint64_t)(uintptr_t)dout, (uint64_t)ldd * os}) >= OA;
-            const int nvec = (int)(vec ? M / V : M);
-            auto run = [&](auto kern, int loads) {
+            // single values against shifted vectors, us, k = 2: 8192 x 4099 bf16 117 and 87, 20000 x 601 72 and 59, 20000 x 301
+            // 40.8 and 40.8, 20000 x 100 13 and 20
+            const bool odd = !whole && rs == 2 && M >= 300;
+            const int nvec = (int)(whole || odd ? M / V : M);
+            auto grid = [&](int loads, int choices) {  // choices: of a block at a time
                 FpRowGrid g = fp_row_grid(c, T, nvec, loads, false);
-                if (T * nvec < (int64_t)c->num_sms * 1024) {  // few tokens: wider blocks, the choices over blocks
+                // few tokens: wider blocks, the choices over blocks (211 x 9648 fp32, k = 2: 18.7 us without, 10.4)
+                if (g.gx < 4u * c->num_sms) {
                     while (g.tpr < MO_GRAD_THREADS && g.tpr * loads < nvec) g.tpr = std::min(MO_GRAD_THREADS, 2 * g.tpr);
                     g.rpb = std::max(1, FP_ROW_THREADS / g.tpr);
                     g.gx = (unsigned)((T + g.rpb - 1) / g.rpb);
-                    g.gy = (unsigned)std::min(k / 2 + (k & 1), 32);
+                    g.gy = (unsigned)std::min((k + choices - 1) / choices, 32);
                 }
-                kern<<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k,
-                                                               nvec, (RT*)drows, lddr, dweights, g.tpr, !vec || dvec);
+                return g;
             };
-            if (!vec)
+            auto run = [&](auto kern, int loads) {
+                const FpRowGrid g = grid(loads, 2);
+                kern<<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k,
+                                                               nvec, (RT*)drows, lddr, dweights, g.tpr, dvec);
+            };
+            if constexpr (sizeof(RT) == 2) {
+                if (odd) {
+                    const FpRowGrid g = grid(1, 1);
+                    moe_grad_odd_kernel<RT, OT, V><<<dim3(g.gx, g.gy), g.threads(), 0, st>>>(
+                        (const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k, (int)M, (RT*)drows, lddr, dweights, g.tpr);
+                    return;
+                }
+            }
+            if (!whole)
                 run(moe_grad_kernel<RT, OT, 1, 4, false>, 4);
             else
                 aligned ? run(moe_grad_kernel<RT, OT, V, 1, false>, 1) : run(moe_grad_kernel<RT, OT, V, 1, true>, 1);

@@ -1012,3 +1012,83 @@ def test_refusals_of_device_tensors(env, monkeypatch, way):
     with pytest.raises(fp.FpError, match="fp_moe_sort") as err:
         ctx.moe_sort(e, 5000, torch.zeros(5001, dtype=torch.int32, device="cuda"), pos)
     assert err.value.code == -2
+
+
+# ---- long rows of odd widths, addresses and pitches -----------------------------------------------------
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,k,K,pad,lead", [(300, 0, 2049, 0, 0), (150, 1, 5121, 3, 1), (300, 3, 1000, 5, 3), (20, 2, 40001, 1, 0), (33, 1, 16385, 0, 0),
+                                            (33, 1, 16391, 2, 1), (40, 2, 8193, 0, 2), (33, 1, 16384, 3, 0), (500, 1, 531, 0, 0)])
+def test_quantize_odd_rows(env, dtype, T, k, K, pad, lead):
+    # to several rows each; rows whose maximum is a multiple of 127 (ties in every type), rows of zeros, of the type's
+    # smallest values, with an infinity or a NaN at either end
+    torch, fp, ctx = env
+    dt = getattr(torch, dtype)
+    rng = np.random.default_rng(K)
+    v = rng.standard_normal((T, K)) * np.exp(rng.standard_normal((T, 1)))
+    for t in range(0, T, 4):  # the halves of 127 x / a, exactly
+        v[t] = np.ldexp(rng.integers(-127, 127, K) + 0.5, int(rng.integers(-6, 6)))
+        v[t, rng.integers(K)] = np.ldexp(127.0, int(np.ceil(np.log2(np.abs(v[t]).max() / 127))))
+    v[1], v[2] = 0.0, float(torch.finfo(dt).smallest_normal) * rng.integers(-8, 8, K) / 8
+    v[3, K - 1], v[5, 0], v[6, K - 1] = math.nan, math.inf, -300.0
+    x, _ = wide(torch, T, K, pad, dt, lead)
+    x.copy_(torch.from_numpy(v).to(dt).cuda())
+    n = T * max(k, 1) + 2
+    q, qb = wide(torch, n, K, pad, torch.int8, lead)
+    before, scale = qb.clone(), torch.full((n,), 5.0, device="cuda")
+    pos = routed(rng, T, k, 4) if k else np.arange(T, dtype=np.int32)[:, None]
+    ctx.quantize_rows(x, q, scale, pos=torch.from_numpy(pos).cuda() if k else None)
+    wq, ws = quantized(x.double().cpu().numpy())
+    want, wscale = np.full((n, K), 7, dtype=np.int8), np.full(n, 5.0, dtype=np.float32)
+    for t in range(T):
+        for p in pos[t]:
+            if p >= 0:
+                want[p], wscale[p] = wq[t], ws[t]
+    assert np.array_equal(q.cpu().numpy(), want)
+    assert np.array_equal(scale.cpu().numpy(), wscale, equal_nan=True)
+    untouched(torch, q, qb, before)
+
+
+@pytest.mark.parametrize("dtype,T,k,K,pad,lead", [("int8", 500, 3, 1500, 0, 5), ("int8", 3, 64, 20001, 0, 0), ("bfloat16", 300, 2, 2049, 3, 1),
+                                                  ("float16", 600, 1, 2049, 1, 0), ("float32", 100, 3, 2049, 2, 1), ("int8", 1200, 2, 1025, 0, 0),
+                                                  ("float32", 2, 40, 30001, 0, 3)])
+def test_dispatch_odd_rows(env, dtype, T, k, K, pad, lead):
+    test_moe_dispatch(env, dtype, K, pad, lead, T, k)
+
+
+@pytest.mark.parametrize("rt,ot", [("bfloat16", "bfloat16"), ("float16", "float32"), ("bfloat16", "float16")])
+@pytest.mark.parametrize("T,k,M,pad,lead", [(260, 3, 4099, 0, 0), (260, 1, 4099, 3, 1), (600, 2, 2055, 1, 3), (130, 5, 8192, 2, 0)])
+@pytest.mark.parametrize("weighted,based", [(True, True), (False, False)])
+def test_combine_odd_rows(env, rt, ot, T, k, M, pad, lead, weighted, based):
+    test_moe_combine(env, rt, ot, T, k, M, pad, lead, weighted, based)
+
+
+@pytest.mark.parametrize("rt,ot", [("bfloat16", "bfloat16"), ("float16", "float32"), ("bfloat16", "float16"), ("float32", "float32")])
+@pytest.mark.parametrize("T,k,M,pad,lead", [(64, 3, 1501, 3, 1), (700, 2, 301, 0, 0), (3, 9, 4099, 0, 0), (900, 1, 607, 2, 5), (5, 2, 9001, 1, 0)])
+def test_grad_odd_rows(env, rt, ot, T, k, M, pad, lead):
+    test_moe_combine_grad(env, rt, ot, T, k, M, pad, lead)
+
+
+@pytest.mark.parametrize("rt", TYPES)
+@pytest.mark.parametrize("T,k,M,pad", [(40, 3, 1501, 0), (700, 2, 304, 3), (9, 2, 100, 0)])
+def test_grad_parts_are_the_whole(env, rt, T, k, M, pad):
+    # one gradient alone has the bits that it has beside the other, at any address of the other
+    torch, fp, ctx = env
+    rng = np.random.default_rng(M)
+    dt = getattr(torch, rt)
+
+    def rows(n, lead=0):
+        return wide(torch, n, M, pad, dt, lead)[0]
+
+    r, g, p = rows(T * k), rows(T), torch.from_numpy(routed(rng, T, k, 4)).cuda()
+    r.copy_(torch.from_numpy(rng.standard_normal(r.shape)).cuda())
+    g.copy_(torch.from_numpy(rng.standard_normal(g.shape)).cuda())
+    w = torch.rand(T, k, device="cuda")
+    dr, dw = rows(T * k), torch.empty(T, k, device="cuda")
+    ctx.moe_combine_grad(g, r, p, w, dr, dw)
+    alone, dw2, dw3 = rows(T * k, 1), torch.empty_like(dw), torch.empty_like(dw)
+    ctx.moe_combine_grad(g, r, p, w, alone)
+    ctx.moe_combine_grad(g, r, p, w, None, dw2)
+    other = rows(T * k, 3)
+    ctx.moe_combine_grad(g, r, p, w, other, dw3)
+    assert torch.equal(alone, dr) and torch.equal(other, dr) and torch.equal(dw2, dw) and torch.equal(dw3, dw)
