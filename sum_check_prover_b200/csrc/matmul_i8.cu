@@ -696,6 +696,8 @@ struct MiRealign {
 constexpr int MI_RE = 4;  // 16-byte pieces of a thread, a block's width apart
 
 __global__ void __launch_bounds__(256) realign_rows_kernel(MiRealign j0, MiRealign j1, int K) {
+    // the product's set-up overlaps the last blocks of this (it waits for their end before it reads)
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const bool second = blockIdx.x >= j0.blocks;
     const MiRealign j = second ? j1 : j0;
     const uint32_t b = blockIdx.x - (second ? j0.blocks : 0), down = b / j.across, c0 = (b - down * j.across) * (256 * MI_RE);
