@@ -22,6 +22,8 @@
 // SPLIT: with fewer tiles than SMs the sum over K of a tile is split among the blocks of a cluster. The
 // blocks exchange their int32 partial sums through distributed shared memory: block d of the cluster
 // finishes the d-th share of the columns. Integer sums have no order, so the split changes no bit.
+// The cluster's barrier is awaited only by the warps that write to the others, and no block waits for another to leave
+// (4384 x 1600, 16 tokens: 6.5 us, with both waits 7.2).
 //
 // What bounds it, and what it takes (B200, repeated calls on changing inputs):
 //   many tokens    the tensor cores: 4096 x 14336 x 4096 157-161 us, 3.0 PTOP/s, 0.9 of twice the measured bf16
@@ -352,6 +354,8 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
         }
     }
+    // the other blocks' barriers are there before anything arrives at them (SPLIT: awaited by those who send)
+    if (SPLIT) asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");
     // what is above overlaps the end of the kernel before this one on the stream; from here on its results are
     // read (with plain loads: an invariant one could be moved up across the wait). The next kernel may be brought
     // onto the SMs that this one leaves.
@@ -413,9 +417,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
     asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-    if (SPLIT || PAIR) {  // the other blocks' barriers are there before anything arrives at them
-        asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;\n" ::: "memory");
-    }
+    if (PAIR) asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;\n" ::: "memory");
     const uint32_t tmem = tmem_base;
     const int total_u = tiles[a.E];  // token tiles; tile (u, m) of channel tile m
     // this block's (SPLIT, PAIR: this cluster's) first tile and its step; SPLIT has one tile per cluster
@@ -538,6 +540,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
         // (53 experts, 1649 tokens, 2992 x 96: 20.7 us, tiles shared 23.5).
         const int qd = warp & 3, group = (warp - 2) >> 2;
         const bool several = (int64_t)total_u * a.mt > walkers;  // some block has more than one tile
+        if (SPLIT) asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory");
         uint32_t tc = 0;
         for (int u = u0, m = mm0; u < total_u; tc++) {
             const MiTokens tk = mi_tokens(first, tiles, a.E, u);
@@ -657,7 +660,10 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
     asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-    if (SPLIT || PAIR)  // no block leaves while another may still write to it or read its operands
+    // no block leaves while another may still write to it or read its operands. SPLIT: a block has had all that the
+    // others write to it before it finishes its share, unless a wait ran out.
+    if (SPLIT && warp < 2) asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory");
+    if (PAIR || (SPLIT && s_abort))
         asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;\n" ::: "memory");
     if (warp == 1) {
         if (PAIR)
@@ -918,8 +924,11 @@ int mi_split(fp_ctx* c, int64_t tiles, int64_t nk) {
 }
 
 // Tiles of 32 tokens where a group has no more (deeper stages); of 128 where all such tiles are on the GPU at
-// once, K split or whole (512 x 4096 x 4096: 16.2 us, pairs 17.7; 256 x 2048 x 8192: 14.2 and 26.1); else pairs
-// (1024 x 4096 x 4096: 18.2 us, tiles of 128 25.1)
+// once, K split or whole (512 x 4096 x 4096: 16.2 us, pairs 17.7; 256 x 2048 x 8192: 14.2 and 26.1), and where a tile is
+// soon done, so that the epilogue counts and a pair's 256 columns stay empty (96 experts, 3722 tokens, 608 x 240: 11.8
+// us, pairs 15.4; 64, 4000, 4096 x 1024: 55 and 60; 64, 6000, 1024 x 1024: 22.9 and 26.2; 802 x 12944 x 128: 15.7 and
+// 16.3); else pairs (1024 x 4096 x 4096: 18.2 us, tiles of 128 25.1; 64, 4000, 4096 x 2048: 96.2 and 97.5; 256 x 16384 x
+// 1024: 11.4 and 11.8)
 int launch_product(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x, int64_t rows, cudaStream_t st) {
     const int64_t mt = (a.M + MI_BM - 1) / MI_BM, nk = (a.K + MI_BK - 1) / MI_BK;
     a.nk = (int32_t)nk;
@@ -930,7 +939,7 @@ int launch_product(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x,
                          : launch_mi<32, false, false>(c, a, w, x, tt, 1, st);
     }
     const int64_t tt = mi_token_tiles(a, 128);
-    if (tt * mt <= c->num_sms) {
+    if (tt * mt <= c->num_sms || nk <= 4 || (nk < 12 && rows < 256)) {
         const int split = mi_split<128>(c, tt * mt, nk);
         return split > 1 ? launch_mi<128, true, false>(c, a, w, x, tt, split, st)
                          : launch_mi<128, false, false>(c, a, w, x, tt, 1, st);
