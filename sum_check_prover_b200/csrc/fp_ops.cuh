@@ -116,12 +116,12 @@ __device__ __forceinline__ void fp_shift16(const uint4& a, const uint4& b, uint3
 }
 
 // 16 bytes from any address: the two aligned 16 bytes that they lie in, shifted. False where those are not
-// both inside the span (the matrix's ends).
+// both inside the span (the matrix's ends). Plain loads: invariant ones may be moved up across a griddepcontrol.wait.
 __device__ __forceinline__ bool fp_load16_any(const void* p, const FpSpan& span, uint32_t (&o)[4]) {
     const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
     const char* q = reinterpret_cast<const char*>(p) - sh;
     if (q < span.lo || q + 32 > span.hi) return false;
-    fp_shift16(__ldg(reinterpret_cast<const uint4*>(q)), __ldg(reinterpret_cast<const uint4*>(q) + 1), sh, o);
+    fp_shift16(reinterpret_cast<const uint4*>(q)[0], reinterpret_cast<const uint4*>(q)[1], sh, o);
     return true;
 }
 

@@ -704,6 +704,7 @@ constexpr int MI_RE = 4;  // 16-byte pieces of a thread, a block's width apart
 __global__ void __launch_bounds__(256) realign_rows_kernel(MiRealign j0, MiRealign j1, int K) {
     // the product's set-up overlaps the last blocks of this (it waits for their end before it reads)
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");  // (the kernel before this one)
     const bool second = blockIdx.x >= j0.blocks;
     const MiRealign j = second ? j1 : j0;
     const uint32_t b = blockIdx.x - (second ? j0.blocks : 0), down = b / j.across, c0 = (b - down * j.across) * (256 * MI_RE);
@@ -723,7 +724,7 @@ __global__ void __launch_bounds__(256) realign_rows_kernel(MiRealign j0, MiReali
         }
         if (j.offsets) {
             const uint32_t e = row / (uint32_t)j.M;
-            if (__ldg(j.offsets + e + 1) <= max(0, __ldg(j.offsets + e))) continue;
+            if (j.offsets[e + 1] <= max(0, j.offsets[e])) continue;
         }
         const int8_t* p = j.src + (int64_t)row * j.ld + first;
         const int lo = max(0, -first), hi = K - first;  // the bytes of the piece inside the row
@@ -805,9 +806,18 @@ int mi_realign(fp_ctx* c, MiOperand& w, MiOperand& x, int K, const int32_t* offs
     }
     int slot;
     fp_op_tic(c, scratch.st, K_REALIGN, 2.0 * (double)bytes, &slot);
-    realign_rows_kernel<<<(unsigned)blocks, 256, 0, scratch.st>>>(job[0], job[1], K);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = scratch.st;
+    cudaLaunchAttribute pdl;
+    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &pdl;
+    cfg.numAttrs = 1;
+    const cudaError_t rc = cudaLaunchKernelEx(&cfg, realign_rows_kernel, job[0], job[1], K);
     fp_toc(c, scratch.st, slot);
-    FP_CUDA(c, cudaGetLastError());
+    FP_CUDA(c, rc);
     return FP_OK;
 }
 
