@@ -806,16 +806,7 @@ int mi_realign(fp_ctx* c, MiOperand& w, MiOperand& x, int K, const int32_t* offs
     }
     int slot;
     fp_op_tic(c, scratch.st, K_REALIGN, 2.0 * (double)bytes, &slot);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(256);
-    cfg.stream = scratch.st;
-    cudaLaunchAttribute pdl;
-    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &pdl;
-    cfg.numAttrs = 1;
-    const cudaError_t rc = cudaLaunchKernelEx(&cfg, realign_rows_kernel, job[0], job[1], K);
+    const cudaError_t rc = fp_launch(realign_rows_kernel, dim3((unsigned)blocks), 256, 0, scratch.st, job[0], job[1], K);
     fp_toc(c, scratch.st, slot);
     FP_CUDA(c, rc);
     return FP_OK;

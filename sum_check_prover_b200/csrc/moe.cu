@@ -40,7 +40,9 @@ __global__ void __launch_bounds__(1024)
     moe_sort_kernel(const int32_t* __restrict__ e, int64_t n, int E, int warps, int32_t* __restrict__ offsets,
                     int32_t* __restrict__ pos) {
     cg::cluster_group cl = cg::this_cluster();
-    const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    unsigned block = cl.block_rank();
+    fp_begin(block);
+    const int C = (int)cl.num_blocks(), rank = (int)block;
     extern __shared__ int32_t ms_smem[];
     int32_t* hist = ms_smem;             // warps x E
     int32_t* tot = hist + warps * E;     // this block's choices of every expert (read by the cluster)
@@ -160,7 +162,9 @@ template <int A, int U>
 __global__ void __launch_bounds__(FP_ROW_THREADS)
     moe_dispatch_kernel(const char* __restrict__ x, int64_t T, int nvec, int64_t ldx, const int32_t* __restrict__ pos,
                         int k, int64_t R, char* __restrict__ rows, int64_t ldr, int tpr) {
-    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    unsigned block = blockIdx.x;
+    fp_begin(block);
+    const int64_t t = (int64_t)block * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
     const char* src = x + t * ldx;
     const int step = tpr * gridDim.y;
@@ -193,7 +197,9 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
 __global__ void __launch_bounds__(FP_ROW_THREADS)
     moe_dispatch_any_kernel(const uint8_t* __restrict__ x, int64_t T, int64_t bytes, int64_t ldx, const int32_t* __restrict__ pos,
                             int k, int64_t R, uint8_t* __restrict__ rows, int64_t ldr, int tpr) {
-    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    unsigned block = blockIdx.x;
+    fp_begin(block);
+    const int64_t t = (int64_t)block * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
     const uint8_t* src = x + t * ldx;
     const FpSpan span = fp_span(x, T, ldx, bytes);
@@ -234,7 +240,7 @@ void launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, i
     const int nvec = (int)(bytes / A);
     constexpr int U = A == 16 ? 2 : 4;
     const FpRowGrid g = fp_row_grid(c, T, nvec, U, true);
-    moe_dispatch_kernel<A, U><<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const char*)x, T, nvec, ldx, pos, k, R,
+    fp_launch(moe_dispatch_kernel<A, U>, dim3(g.gx, g.gy), g.threads(), 0, st, (const char*)x, T, nvec, ldx, pos, k, R,
                                                                         (char*)rows, ldr, g.tpr);
 }
 
@@ -250,7 +256,9 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
     moe_combine_kernel(const RT* __restrict__ rows, int64_t R, int64_t ldr, const int32_t* __restrict__ pos,
                        const float* __restrict__ w, const OT* base, int64_t ldb, int64_t T, int k, int nvec, OT* out,
                        int64_t ldo, int tpr) {
-    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    unsigned block = blockIdx.x;
+    fp_begin(block);
+    const int64_t t = (int64_t)block * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
     const int step = tpr * gridDim.y;
     for (int c = threadIdx.x % tpr + tpr * blockIdx.y; c < nvec; c += U * step) {
@@ -305,7 +313,9 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
     moe_combine_odd_kernel(const RT* __restrict__ rows, int64_t R, int64_t ldr, const int32_t* __restrict__ pos,
                            const float* __restrict__ w, const OT* base, int64_t ldb, int64_t T, int k, int M, OT* out,
                            int64_t ldo, int tpr) {
-    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    unsigned block = blockIdx.x;
+    fp_begin(block);
+    const int64_t t = (int64_t)block * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (t >= T) return;
     const int step = tpr * gridDim.y, at = threadIdx.x % tpr;
     OT* o = out + t * ldo;
@@ -373,9 +383,11 @@ __global__ void __launch_bounds__(MO_GRAD_THREADS)
     moe_grad_kernel(const OT* __restrict__ dout, int64_t ldd, const RT* __restrict__ rows, int64_t R, int64_t ldr,
                     const int32_t* __restrict__ pos, const float* __restrict__ w, int64_t T, int k, int nvec,
                     RT* __restrict__ drows, int64_t lddr, float* __restrict__ dw, int tpr, bool dvec) {
+    unsigned block = blockIdx.x;
+    fp_begin(block);
     __shared__ float red[2][32];
     const int sub = threadIdx.x / tpr, tt = threadIdx.x % tpr, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + sub;
+    const int64_t t = (int64_t)block * (blockDim.x / tpr) + sub;
     const bool live = t < T;
     const FpRow<OT, V, ANY> g(dout + (live ? t : 0) * ldd, fp_span(dout, T, ldd, (int64_t)nvec * V));
     const FpSpan rspan = fp_span(rows, R, ldr, (int64_t)nvec * V);
@@ -457,9 +469,11 @@ __global__ void __launch_bounds__(MO_GRAD_THREADS)
     moe_grad_odd_kernel(const OT* __restrict__ dout, int64_t ldd, const RT* __restrict__ rows, int64_t R, int64_t ldr,
                         const int32_t* __restrict__ pos, const float* __restrict__ w, int64_t T, int k, int M,
                         RT* __restrict__ drows, int64_t lddr, float* __restrict__ dw, int tpr) {
+    unsigned block = blockIdx.x;
+    fp_begin(block);
     __shared__ float red[32];
     const int sub = threadIdx.x / tpr, tt = threadIdx.x % tpr, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / tpr) + sub;
+    const int64_t t = (int64_t)block * (blockDim.x / tpr) + sub;
     const bool live = t < T;
     const OT* g = dout + (live ? t : 0) * ldd;
     const FpSpan gspan = fp_span(dout, T, ldd, M), rspan = fp_span(rows, R, ldr, M);
@@ -568,12 +582,14 @@ int fp_moe_sort(fp_ctx* c, const int32_t* e, int64_t n, int E, int32_t* offsets,
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];  // (as fp_launch, in a cluster)
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)blocks;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     int slot;
     fp_op_tic(c, st, K_MOE_SORT, 8.0 * (double)n + 4.0 * E, &slot);
     const cudaError_t rc = cudaLaunchKernelEx(&cfg, moe_sort_kernel, e, n, E, warps, offsets, pos);
@@ -609,7 +625,7 @@ int fp_moe_dispatch(fp_ctx* c, const void* x, int64_t T, int64_t row_bytes, int6
     if (al <= 4 && row_bytes >= 1024 * al && T * k * row_bytes >= (1 << 21)) {
         const FpRowGrid g = fp_row_grid(c, T, row_bytes / 16, 1, true);
         const int64_t gz = std::max<int64_t>(1, std::min<int64_t>(k, 4 * (int64_t)c->num_sms / ((int64_t)g.gx * g.gy)));
-        moe_dispatch_any_kernel<<<dim3(g.gx, g.gy, (unsigned)gz), g.threads(), 0, st>>>(
+        fp_launch(moe_dispatch_any_kernel, dim3(g.gx, g.gy, (unsigned)gz), g.threads(), 0, st,
             (const uint8_t*)x, T, row_bytes, ldx, pos, k, R, (uint8_t*)rows, ldr, g.tpr);
     } else if (al >= 16)
         launch_dispatch<16>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
@@ -664,7 +680,7 @@ int fp_moe_combine(fp_ctx* c, const void* rows, int rows_type, int64_t R, int64_
             const int nvec = (int)(vec || odd ? M / V : M);
             auto run = [&](auto kern, int loads, int width) {
                 const FpRowGrid g = fp_row_grid(c, T, nvec, loads, true);
-                kern<<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const RT*)rows, R, ldr, pos, weights, (const OT*)base, ldb, T,
+                fp_launch(kern, dim3(g.gx, g.gy), g.threads(), 0, st, (const RT*)rows, R, ldr, pos, weights, (const OT*)base, ldb, T,
                                                                k, width, (OT*)out, ldo, g.tpr);
             };
             if constexpr (sizeof(RT) == 2) {
@@ -737,13 +753,13 @@ int fp_moe_combine_grad(fp_ctx* c, const void* dout, int out_type, int64_t ldd, 
             };
             auto run = [&](auto kern, int loads) {
                 const FpRowGrid g = grid(loads, 2);
-                kern<<<dim3(g.gx, g.gy), g.threads(), 0, st>>>((const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k,
+                fp_launch(kern, dim3(g.gx, g.gy), g.threads(), 0, st, (const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k,
                                                                nvec, (RT*)drows, lddr, dweights, g.tpr, dvec);
             };
             if constexpr (sizeof(RT) == 2) {
                 if (odd) {
                     const FpRowGrid g = grid(1, 1);
-                    moe_grad_odd_kernel<RT, OT, V><<<dim3(g.gx, g.gy), g.threads(), 0, st>>>(
+                    fp_launch(moe_grad_odd_kernel<RT, OT, V>, dim3(g.gx, g.gy), g.threads(), 0, st,
                         (const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k, (int)M, (RT*)drows, lddr, dweights, g.tpr);
                     return;
                 }

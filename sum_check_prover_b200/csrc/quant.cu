@@ -142,8 +142,10 @@ template <typename T, int V, int NV>
 __global__ void __launch_bounds__(256, 4)
     quant_rows_kernel(const T* __restrict__ x, int64_t rows, int K, int64_t ldx, const int32_t* __restrict__ pos, int k,
                       int64_t R, int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale, int tpr) {
+    unsigned block = blockIdx.x;
+    fp_begin(block);
     const int sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + sub;
+    const int64_t row = (int64_t)block * (blockDim.x / tpr) + sub;
     const bool live = row < rows;
     const T* xr = x + (live ? row : 0) * ldx;
     const int nvec = live ? K / V : 0;
@@ -217,9 +219,11 @@ template <typename T, int V>
 __global__ void __launch_bounds__(256, 4)
     quant_odd_rows_kernel(const T* __restrict__ x, int64_t rows, int K, int64_t ldx, const int32_t* __restrict__ pos,
                           int k, int64_t R, int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale, int tpr) {
+    unsigned block = blockIdx.x;
+    fp_begin(block);
     extern __shared__ uint4 st[];
     const int sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + sub;
+    const int64_t row = (int64_t)block * (blockDim.x / tpr) + sub;
     const bool live = row < rows;
     const FpRow<T, V, true> src(x + (live ? row : 0) * ldx, fp_span(x, rows, ldx, K));
     const int len = live ? K : 0, nvec = len / V, rest = len % V;  // the last values of a row, one for each of its threads
@@ -310,7 +314,7 @@ void launch_quant(const fp_ctx* c, const void* x, int64_t T_, int64_t K, int64_t
     const int threads = std::max(128 / tpr, 1) * tpr;
     const unsigned grid = (unsigned)((T_ + threads / tpr - 1) / (threads / tpr));
     auto run = [&](auto kern, int smem) {
-        kern<<<grid, threads, smem, st>>>((const T*)x, T_, (int)K, ldx, pos, k, R, q, ldq, scale, tpr);
+        fp_launch(kern, grid, threads, smem, st, (const T*)x, T_, (int)K, ldx, pos, k, R, q, ldq, scale, tpr);
     };
     if (plain)
         run(quant_rows_kernel<T, V, QR_LOADS>, 0);

@@ -1092,3 +1092,42 @@ def test_grad_parts_are_the_whole(env, rt, T, k, M, pad):
     other = rows(T * k, 3)
     ctx.moe_combine_grad(g, r, p, w, other, dw3)
     assert torch.equal(alone, dr) and torch.equal(other, dr) and torch.equal(dw2, dw) and torch.equal(dw3, dw)
+
+
+@pytest.mark.parametrize("T,K", [(3, 64), (200, 1001), (2000, 5120)])
+def test_calls_follow_one_another(env, T, K):
+    # kernels come onto the SMs before the one in front of them has ended, and read and write only after it: the same
+    # buffers written, read and written again by calls and by torch, without a wait in between
+    torch, fp, ctx = env
+    k, E, n = 2, 4, 24
+    g = torch.Generator(device="cuda").manual_seed(T)
+    src = [torch.randn(T, K, generator=g, device="cuda").bfloat16() for _ in range(4)]
+    e = [torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32) for _ in range(3)]
+    w = torch.rand(T, k, generator=g, device="cuda")
+
+    def run(wait):
+        x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+        off, pos = torch.zeros(E + 1, dtype=torch.int32, device="cuda"), torch.zeros(T, k, dtype=torch.int32, device="cuda")
+        rows, q, sc = torch.zeros(T * k, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, K, dtype=torch.int8, device="cuda"), torch.zeros(T, device="cuda")
+        out, dw, dr = torch.zeros_like(x), torch.zeros(T, k, device="cuda"), torch.zeros_like(rows)
+        kept = []
+        torch.cuda.synchronize()
+        for i in range(n):
+            for call in (lambda: x.copy_(src[i % 4]),
+                         lambda: ctx.moe_sort(e[i % 3], E, off, pos),
+                         lambda: ctx.moe_dispatch(x, pos, rows),
+                         lambda: ctx.moe_combine(rows, pos, x, weights=w, base=x),
+                         lambda: ctx.quantize_rows(x, q, sc),
+                         lambda: ctx.moe_sort(e[(i + 1) % 3], E, off, pos),
+                         lambda: ctx.moe_combine_grad(x, rows, pos, w, dr, dw),
+                         lambda: ctx.moe_dispatch(x, pos, rows),
+                         lambda: ctx.moe_combine(dr, pos, out),
+                         lambda: kept.append([t.clone() for t in (q, sc, out, dw, rows)]) if i % 8 == 7 else None):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        return kept
+
+    for one, other in zip(run(True), run(False)):
+        for a, b in zip(one, other):
+            assert torch.equal(a, b)
