@@ -924,7 +924,11 @@ int mi_split(fp_ctx* c, int64_t tiles, int64_t nk) {
     return 1;
 }
 
-// Tiles of 32 tokens where a group has no more (deeper stages); of 128 where all such tiles are on the GPU at
+// Tiles of 32 tokens where a group has no more (deeper stages), and where all of them are on the GPU at once: then more
+// SMs share the epilogue, for reading the weights several times (102 x 2895 x 368: 5.1 us, tiles of 128 7.1; 128 x 1024 x
+// 1024: 5.9 and 7.5; 128 x 4096 x 2048: 8.1 and 9.2). With a longer K only if a block has no more bytes to load, a
+// k-tile's 20 KB against 32, with K split or not (100 x 512 x 4096: 7.9 and 9.8; 64 x 2048 x 8192: 10.3 and 10.8; but 96 x
+// 6000 x 4096: 12.9 and 11.9, 128 x 4096 x 8192: 20.8 and 14.5). Tiles of 128 where all such tiles are on the GPU at
 // once, K split or whole (512 x 4096 x 4096: 16.2 us, pairs 17.7; 256 x 2048 x 8192: 14.2 and 26.1), and where a tile is
 // soon done, so that the epilogue counts and a pair's 256 columns stay empty (96 experts, 3722 tokens, 608 x 240: 11.8
 // us, pairs 15.4; 64, 4000, 4096 x 1024: 55 and 60; 64, 6000, 1024 x 1024: 22.9 and 26.2; 802 x 12944 x 128: 15.7 and
@@ -933,15 +937,13 @@ int mi_split(fp_ctx* c, int64_t tiles, int64_t nk) {
 int launch_product(fp_ctx* c, MiArgs& a, const MiOperand& w, const MiOperand& x, int64_t rows, cudaStream_t st) {
     const int64_t mt = (a.M + MI_BM - 1) / MI_BM, nk = (a.K + MI_BK - 1) / MI_BK;
     a.nk = (int32_t)nk;
-    if (rows <= 32) {
-        const int64_t tt = mi_token_tiles(a, 32);
-        const int split = mi_split<32>(c, tt * mt, nk);
-        return split > 1 ? launch_mi<32, true, false>(c, a, w, x, tt, split, st)
-                         : launch_mi<32, false, false>(c, a, w, x, tt, 1, st);
-    }
-    const int64_t tt = mi_token_tiles(a, 128);
+    const int64_t tt = mi_token_tiles(a, 128), narrow = mi_token_tiles(a, 32);
+    const int split = mi_split<128>(c, tt * mt, nk), nsplit = mi_split<32>(c, narrow * mt, nk);
+    const bool fits = narrow * mt <= c->num_sms;
+    if (rows <= 32 || (fits && (nk <= 16 || 20 * ((nk + nsplit - 1) / nsplit) <= 32 * ((nk + split - 1) / split))))
+        return nsplit > 1 ? launch_mi<32, true, false>(c, a, w, x, narrow, nsplit, st)
+                          : launch_mi<32, false, false>(c, a, w, x, narrow, 1, st);
     if (tt * mt <= c->num_sms || nk <= 4 || (nk < 12 && rows < 256)) {
-        const int split = mi_split<128>(c, tt * mt, nk);
         return split > 1 ? launch_mi<128, true, false>(c, a, w, x, tt, split, st)
                          : launch_mi<128, false, false>(c, a, w, x, tt, 1, st);
     }
