@@ -1,6 +1,6 @@
 // The binding's short way for the layer operators: a decode step makes several calls of a few microseconds, of
 // which the interpreter's checks of five tensors and the conversion of a dozen arguments took half (us a call, the
-// methods' way and this one: quantised rows 5.9 and 3.0, combine 7.7 and 3.0, gradients 8.4 and 3.2).
+// methods' way and this one: quantised rows 5.4 and 2.4, combine 7.2 and 2.1, gradients 8.1 and 2.5).
 //
 // Each function here takes what the method of the same name takes, reads the tensors' addresses, sizes and pitches
 // directly and makes the C call; it returns the call's status. Whatever it does not know for sure to be right

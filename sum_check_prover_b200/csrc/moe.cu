@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
 // row, x shifted to it (and read for every choice, from L1 after the first), the bytes before and behind one by one.
 // blockIdx.z: a share of the choices. 8192 rows of 5121 bf16 to two rows each, 252 MB, take 48 us, 5.2 TB/s.
 __global__ void __launch_bounds__(FP_ROW_THREADS)
-    moe_dispatch_any_kernel(const uint8_t* __restrict__ x, int64_t T, int64_t bytes, int64_t ldx, const int32_t* __restrict__ pos,
-                            int k, int64_t R, uint8_t* __restrict__ rows, int64_t ldr, int tpr) {
+    moe_dispatch_any_kernel(const uint8_t* __restrict__ x, int64_t T, int64_t bytes, int64_t ldx,
+                            const int32_t* __restrict__ pos, int k, int64_t R, uint8_t* __restrict__ rows, int64_t ldr, int tpr) {
     unsigned block = blockIdx.x;
     fp_begin(block);
     const int64_t t = (int64_t)block * (blockDim.x / tpr) + threadIdx.x / tpr;
@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
         const int64_t p = __ldg(pos + t * k + j);
         if (p < 0 || p >= R) continue;
         uint8_t* dst = rows + p * ldr;
-        const int head = (int)min((int64_t)(-reinterpret_cast<uintptr_t>(dst) & 15), bytes), nvec = (int)((bytes - head) / 16);
+        const int head = (int)min((int64_t)(-reinterpret_cast<uintptr_t>(dst) & 15), bytes);
+        const int nvec = (int)((bytes - head) / 16);
         if (blockIdx.y == 0) {
             const int tail = (int)(bytes - head) & 15;
             if (at < head) dst[at] = src[at];
@@ -411,7 +412,8 @@ __global__ void __launch_bounds__(MO_GRAD_THREADS)
                 for (int j = 0; j < 2; j++)
 #pragma unroll
                     for (int u = 0; u < U; u++)
-                        if (p[j] >= 0 && c + u * tpr < nvec) v[j][u] = FpRow<RT, V, ANY>(rows + p[j] * ldr, rspan).get(c + u * tpr);
+                        if (p[j] >= 0 && c + u * tpr < nvec)
+                            v[j][u] = FpRow<RT, V, ANY>(rows + p[j] * ldr, rspan).get(c + u * tpr);
             }
 #pragma unroll
             for (int j = 0; j < 2; j++) {

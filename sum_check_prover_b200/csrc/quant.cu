@@ -19,7 +19,6 @@
 
 namespace {
 
-
 constexpr int QR_LOADS = 8;              // vectors of a row that a thread keeps in registers
 constexpr float QR_MAGIC = 12582912.0f;  // 1.5 * 2^23: t + it has the nearest integer to t in its low bits
 constexpr float QR_NEAR = 0.5f - 3.0517578e-5f;
@@ -135,9 +134,9 @@ __device__ __forceinline__ float quant_scale(const QuantRow& r, float amax) {
     return r.bad ? __uint_as_float(0x7fc00000u) : amax / 127.0f;
 }
 
-// One row per `tpr` threads (a multiple of 32 that divides the block). V: elements per load; a thread keeps the first NV vectors it reads in registers, and reads what is beyond them a
-// second time. x's address and pitch are
-// multiples of 16 bytes, K, q's address and its pitch of V.
+// One row per `tpr` threads (a multiple of 32 that divides the block). V: elements per load; a thread keeps the first
+// NV vectors it reads in registers, and reads what is beyond them a second time. x's address and pitch are multiples of V
+// elements, K, q's address and its pitch of V.
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(256, 4)
     quant_rows_kernel(const T* __restrict__ x, int64_t rows, int K, int64_t ldx, const int32_t* __restrict__ pos, int k,
@@ -286,7 +285,8 @@ __global__ void __launch_bounds__(256, 4)
             if (p < 0 || p >= R) continue;
             if (t == 0 && c0 == 0) scale[p] = quant_scale(r, amax);
             int8_t* d = q + p * ldq + c0 * V;
-            const int head = min((int)(-reinterpret_cast<uintptr_t>(d) & 15), n), words = (n - head) / 16, tail = (n - head) & 15;
+            const int head = min((int)(-reinterpret_cast<uintptr_t>(d) & 15), n);
+            const int words = (n - head) / 16, tail = (n - head) & 15;
             if (t < head) d[t] = (int8_t)mine[t];
             if (t < tail) d[n - tail + t] = (int8_t)mine[n - tail + t];
             for (int v = t; v < words; v += tpr) {
@@ -310,7 +310,8 @@ void launch_quant(const fp_ctx* c, const void* x, int64_t T_, int64_t K, int64_t
     const int64_t nvec = single ? K : K / V;
     // a few warps hold a row in registers, so that many rows are in flight; few rows: a vector a thread
     int tpr = 32;
-    while (tpr < 256 && ((int64_t)tpr * (single ? 2 * QR_LOADS : QR_LOADS) < nvec || (T_ * tpr < (int64_t)c->num_sms * 256 && tpr < nvec))) tpr += 32;
+    const int loads = single ? 2 * QR_LOADS : QR_LOADS;
+    while (tpr < 256 && ((int64_t)tpr * loads < nvec || (T_ * tpr < (int64_t)c->num_sms * 256 && tpr < nvec))) tpr += 32;
     const int threads = std::max(128 / tpr, 1) * tpr;
     const unsigned grid = (unsigned)((T_ + threads / tpr - 1) / (threads / tpr));
     auto run = [&](auto kern, int smem) {
