@@ -546,9 +546,19 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
             const MiTokens tk = mi_tokens(first, tiles, a.E, u);
             const uint32_t slot = tc % SLOTS;
             const bool alone = !SPLIT && several && tk.cols <= 64;  // a group's own tile
+            // Every warp arrives once for every tile, the four that pass a tile over when they have seen its
+            // accumulator's phase: the slot's next phase then cannot end before all eight have seen this one, and no
+            // warp loses count of the phases.
+            const auto leave_slot = [&] {
+                if (lane != 0) return;
+                if (PAIR)
+                    mi_arrive_at(mi_smem(&accempty[slot]), 0, 1);
+                else
+                    mi_arrive(mi_smem(&accempty[slot]), 1);
+            };
             if (alone && (int)(tc & 1) != group) {
-                // (the other's; the wait keeps this warp's count of the barrier's phases)
                 if (!mi_wait_warp(mi_smem(&accfull[slot]), (tc / SLOTS) & 1u, &s_abort, err)) break;
+                leave_slot();
                 u += du, m += dm;
                 if (m >= a.mt) m -= a.mt, u++;
                 continue;
@@ -645,13 +655,7 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
             }
             asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
             __syncwarp();
-            if (lane == 0) {
-                // (the four warps of a tile of their own arrive for the other four)
-                if (PAIR)
-                    mi_arrive_at(mi_smem(&accempty[slot]), 0, alone ? 2 : 1);
-                else
-                    mi_arrive(mi_smem(&accempty[slot]), alone ? 2 : 1);
-            }
+            leave_slot();
             u += du, m += dm;
             if (m >= a.mt) m -= a.mt, u++;
         }

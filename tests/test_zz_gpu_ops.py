@@ -1131,3 +1131,97 @@ def test_calls_follow_one_another(env, T, K):
     for one, other in zip(run(True), run(False)):
         for a, b in zip(one, other):
             assert torch.equal(a, b)
+
+
+# ---- products of many tiles: blocks that take several, one after the other -----------------------------
+
+def ragged(n, lo, hi, seed, empty=0.0):
+    """n groups of lo to hi rows, some of them without any."""
+    rng = np.random.default_rng(seed)
+    return [int(c) for c in rng.integers(lo, hi + 1, n) * (rng.random(n) >= empty)]
+
+
+# tokens or groups, channels, K, pitches beyond the row (x, y)
+MANY_TILES = {
+    # pairs of blocks, 256 channels by 256 tokens: the last channel tile is the first block's alone, the last tokens are no
+    # multiple of 32
+    "pairs": (700, 6000, 640, 0, 0),
+    "pairs, odd rows of y": (603, 6001, 768, 16, 3),
+    "pairs, long K": (900, 5000, 2048, 0, 8),
+    "pairs, ragged groups": ([300, 1, 0, 64, 513, 33, 257, 340, 65, 0], 2500, 1536, 0, 0),
+    "pairs, groups of up to 64": (ragged(40, 36, 64, 1), 1500, 1536, 0, 0),
+    "pairs, odd pitches": ([500, 64, 1, 535], 2000, 1541, 3, 5),
+    # tiles of 128 tokens, with main loops of a single k-tile
+    "128, groups of up to 64, short K": (ragged(64, 33, 64, 2), 600, 128, 0, 0),
+    "128, all sizes, short K": (ragged(40, 0, 300, 3, 0.2), 900, 112, 0, 4),
+    "128, one group": (4000, 2050, 100, 12, 0),
+    # tiles of 32
+    "32, groups of up to 16": (ragged(100, 0, 16, 4), 1000, 128, 0, 0),
+    "32, groups of up to 16, long K": (ragged(60, 1, 16, 5), 700, 2064, 0, 1),
+    # weights read by classes of rows
+    "classes, short K": (ragged(30, 1, 60, 6), 2500, 65, 0, 0),
+    "classes, two of them": (ragged(30, 20, 64, 7), 2000, 520, 0, 3),
+}
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name", MANY_TILES)
+def test_matmul_many_tiles(env, name, dtype):
+    # small tiles alternate between the two halves of a block's epilogue; a sum's bits hang on nothing but the inputs
+    torch, fp, ctx = env
+    counts, M, K, padx, pady = MANY_TILES[name]
+    E, ends, off = 0, None, None
+    N = counts
+    if not isinstance(counts, int):
+        E, N, ends = len(counts), sum(counts) + 2, np.concatenate([[0], np.cumsum(counts)])
+        off = torch.from_numpy(ends.astype(np.int32)).cuda()
+    w, x, ws, xs, y, yb = product_case(torch, N, M, K, E, dtype, 7 * M + K, padx=padx, pady=pady)
+    y.fill_(7)
+    before = yb.clone()
+    ctx.matmul_i8(w, x, y, ws, xs, offsets=off)
+    check_product(torch, w, x, ws, xs, y, ends)
+    if E:
+        assert bool((y[N - 2:] == 7).all())
+    untouched(torch, y, yb, before)
+    first = y.clone()
+    for _ in range(8):
+        y.fill_(7)
+        ctx.matmul_i8(w, x, y, ws, xs, offsets=off)
+        assert torch.equal(y, first)
+
+
+@pytest.mark.parametrize("T,k,E,K,M", [(1400, 1, 8, 1024, 2500), (2000, 1, 40, 1536, 1500), (1200, 2, 64, 128, 600), (20, 3, 40, 256, 900),
+                                       (300, 2, 30, 520, 1301), (3, 1, 1, 4096, 640)])
+def test_products_follow_other_calls(env, T, k, E, K, M):
+    # activations quantised, multiplied and combined over and over into the same buffers, without a wait in between
+    torch, fp, ctx = env
+    g = torch.Generator(device="cuda").manual_seed(T + M)
+    src = [torch.randn(T, K, generator=g, device="cuda").bfloat16() for _ in range(3)]
+    e = [torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32) for _ in range(2)]
+    w = torch.randint(-128, 128, (E, M, K), generator=g, device="cuda", dtype=torch.int8)
+    ws, wt = torch.rand(E, M, generator=g, device="cuda") * 1e-3, torch.rand(T, k, generator=g, device="cuda")
+
+    def run(wait):
+        x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+        off, pos = torch.zeros(E + 1, dtype=torch.int32, device="cuda"), torch.zeros(T, k, dtype=torch.int32, device="cuda")
+        q, sc = torch.zeros(T * k, K, dtype=torch.int8, device="cuda"), torch.zeros(T * k, device="cuda")
+        y, out = torch.zeros(T * k, M, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, M, device="cuda")
+        kept = []
+        torch.cuda.synchronize()
+        for i in range(12):
+            for call in (lambda: x.copy_(src[i % 3]),
+                         lambda: ctx.moe_sort(e[i % 2], E, off, pos),
+                         lambda: ctx.quantize_rows(x, q, sc, pos=pos),
+                         lambda: ctx.matmul_i8(w, q, y, ws, sc, offsets=off),
+                         lambda: ctx.moe_combine(y, pos, out, weights=wt),
+                         lambda: ctx.matmul_i8(w, q, y, ws, sc, offsets=off),
+                         lambda: ctx.moe_combine(y, pos, out, weights=wt, base=out),
+                         lambda: y.zero_(),
+                         lambda: kept.append(out.clone()) if i % 4 == 3 else None):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        return kept
+
+    for a, b in zip(run(True), run(False)):
+        assert bool(a.any()) and torch.equal(a, b)
