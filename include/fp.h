@@ -752,13 +752,15 @@ int fp_exp_table(int32_t* out);
  * their experts and back ("How fast can FlashProve go", 2 Background, the note on MoE layers).
  *
  * All of them: device pointers on the context's device, every buffer the caller's, nothing
- * allocated (but for fp_matmul_i8's odd pitches). The kernels are queued on `stream` and the call returns without waiting, so that calls
- * may be captured into a CUDA graph; buffers stay alive and unchanged until the stream has passed
- * the call. The caller's current device is left as it was. Calls on different streams, and graphs
- * that hold them, share no memory of the library's. Pitches are in elements (bytes where said) from
- * row to row, not below the row's length; a single row's is not looked at. Inputs may not overlap
- * outputs unless said. Errors: FP_ERR_ARG (null or misaligned pointer, bad type), FP_ERR_SHAPE,
- * FP_ERR_CUDA.
+ * allocated (but for fp_matmul_i8's odd pitches). The kernels are queued on `stream` and the call
+ * returns without waiting, so that calls may be captured into a CUDA graph; buffers stay alive and
+ * unchanged until the stream has passed the call, and the context outlives the graphs that hold its
+ * calls. The caller's current device is left as it was. Calls on different streams, and graphs that
+ * hold them, share no memory of the library's but the word of fp_ops_status. Pitches are in elements
+ * (bytes where said) from row to row, not below the row's length; a single row's is not looked at.
+ * Inputs may not overlap outputs unless said. Errors: FP_ERR_ARG (null or misaligned pointer, bad
+ * type), FP_ERR_SHAPE, FP_ERR_CUDA; FP_ERR_TIMEOUT, from whichever of them is called next and without
+ * queueing its kernels, after a bounded wait of an earlier call ran out on the device.
  */
 enum { FP_F32 = 0, FP_F16 = 1, FP_BF16 = 2 }; /* types of real values */
 
@@ -792,7 +794,7 @@ int fp_quantize_rows(fp_ctx* ctx, const void* x, int x_type, int64_t T, int64_t 
  * copied (of weights the experts that have rows; none where few tokens meet them) to rows that are, in
  * stream-ordered memory of the context, which keeps it for later calls (FP_ERR_OOM if there is none);
  * inside a graph it is the graph's. The kernel's waits are bounded: should one run
- * out, the next call on the context returns FP_ERR_TIMEOUT (once) and the earlier y is not valid.
+ * out, the earlier y is not valid, and fp_ops_status or the next call of an operator says so.
  */
 int fp_matmul_i8(fp_ctx* ctx, const int8_t* w, int64_t ldw, const float* w_scale, int E, int64_t M, int64_t K,
                  const int8_t* x, int64_t ldx, const float* x_scale, int64_t N, const int32_t* offsets, void* y,
@@ -836,6 +838,20 @@ int fp_moe_combine(fp_ctx* ctx, const void* rows, int rows_type, int64_t R, int6
 int fp_moe_combine_grad(fp_ctx* ctx, const void* dout, int out_type, int64_t ldd, const void* rows, int rows_type,
                         int64_t R, int64_t ldr, const int32_t* pos, const float* weights, int64_t T, int k, int64_t M,
                         void* drows, int64_t lddr, float* dweights, void* stream);
+
+/*
+ * Whether a bounded wait of the operators above ran out on the device: FP_ERR_TIMEOUT, once (whichever call reports it
+ * clears it), else FP_OK. It waits for nothing: call it when the stream has been synchronised, after the last operator
+ * of a program or after a graph's replay, for which no later call would say so.
+ */
+int fp_ops_status(fp_ctx* ctx);
+
+/*
+ * Self-test of those waits: queues a kernel that waits a short time for a barrier that nothing arrives at, gives up
+ * and says so as the product's kernel would. fp_ops_status or the next operator then reports it; the context stays
+ * usable.
+ */
+int fp_ops_selftest(fp_ctx* ctx, void* stream);
 
 /*
  * Self-test of the bounded device waits. The sum-check kernels stay resident

@@ -141,6 +141,8 @@ def lib():
     L.fp_moe_dispatch.argtypes = [vp, vp, i64, i64, i64, vp, i32, i64, vp, i64, vp]
     L.fp_moe_combine.argtypes = [vp, vp, i32, i64, i64, vp, vp, vp, i64, i64, i32, i64, vp, i32, i64, vp]
     L.fp_moe_combine_grad.argtypes = [vp, vp, i32, i64, vp, i32, i64, i64, vp, vp, i64, i32, i64, vp, i64, vp, vp]
+    L.fp_ops_status.argtypes = [vp]
+    L.fp_ops_selftest.argtypes = [vp, vp]
     L.fp_ctx_set_profiling.argtypes = [vp, i32]
     L.fp_session_selftest.argtypes = [vp, vp]
     L.fp_host_stats.argtypes = [vp, C.POINTER(C.c_double)]
@@ -1205,6 +1207,16 @@ class Context:
                                              self._op_stream(stream))
         if rc:
             self._check(rc, "fp_moe_combine_grad")
+
+    def ops_status(self) -> None:
+        """Raise FpError (code -4, once) if a bounded wait of the operators above ran out on the device, so that an
+        earlier matmul_i8's y is not valid. The next operator raises it too; this is for a program's last one and for
+        graphs' replays. It waits for nothing: synchronise the stream first."""
+        self._check(self._L.fp_ops_status(self.h), "fp_ops_status")
+
+    def ops_selftest(self, stream=None) -> None:
+        """Queue a kernel whose bounded wait runs out, for ops_status or the next operator to report."""
+        self._check(self._L.fp_ops_selftest(self.h, self._op_stream(stream)), "fp_ops_selftest")
 
     def last_point(self):
         """(r_row, rho) of the last matmul section proven with this context (host integers)."""

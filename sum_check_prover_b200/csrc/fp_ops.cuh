@@ -29,6 +29,15 @@ struct FpDeviceScope {
     FpDeviceScope& operator=(const FpDeviceScope&) = delete;
 };
 
+// What a wait that ran out in an earlier call left: FP_ERR_TIMEOUT, once. Every operator asks before it queues anything.
+static inline int fp_op_pending(fp_ctx* c, const char* what) {
+    if (!c->mb->op_err) return FP_OK;
+    c->mb->op_err = 0;
+    return fp_fail(c, FP_ERR_TIMEOUT,
+                   std::string(what) + ": a wait of an earlier fp_matmul_i8 ran out on the device; its y is not valid, nor what "
+                                       "was made of it since");
+}
+
 static inline int fp_type_size(int type) { return type == FP_F32 ? 4 : (type == FP_F16 || type == FP_BF16) ? 2 : 0; }
 
 // fp_tic for an operator: a launch that is being captured into a graph is counted, not timed (its

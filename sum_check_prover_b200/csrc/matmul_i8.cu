@@ -53,7 +53,7 @@ constexpr int MI_MAX_STAGES = 12;
 constexpr int MI_SMEM = 200 * 1024;         // dynamic shared memory of a block that has its SM alone
 constexpr int MI_EPI_WARPS = 8;
 constexpr int MI_THREADS = 32 * (2 + MI_EPI_WARPS);
-constexpr uint32_t MI_WAIT_LIMIT = 1u << 24;
+constexpr uint32_t MI_WAIT_LIMIT = 1u << 24;  // polls, 4 us each while nothing comes: about a minute
 
 __host__ __device__ constexpr int mi_box_rows(int bn) { return bn >= 256 ? 64 : 32; }  // rows of a token box
 
@@ -110,8 +110,9 @@ __device__ __forceinline__ void mi_bar_init(uint64_t* b, int count) {
 
 // one bounded wait for a phase; false if it ran out or another role has aborted
 template <bool CLUSTER>
-__device__ __forceinline__ bool mi_wait_scope(uint32_t bar, uint32_t parity, volatile int* abort, volatile uint64_t* err) {
-    for (uint32_t it = 0; it < MI_WAIT_LIMIT; it++) {
+__device__ __forceinline__ bool mi_wait_scope(uint32_t bar, uint32_t parity, volatile int* abort, volatile uint64_t* err,
+                                              uint32_t limit = MI_WAIT_LIMIT) {
+    for (uint32_t it = 0; it < limit; it++) {
         uint32_t ok;
         if (CLUSTER)
             asm volatile(
@@ -827,6 +828,18 @@ int mi_classes(const MiOperand& w, int64_t E, int64_t M, int64_t N, int64_t rows
     return M >= 4 * classes && classes * N <= std::min(E, N) * M / 4 ? classes : 0;
 }
 
+// (fp_ops_selftest) a wait for a barrier that nothing arrives at: a second one has the abort flag to end it
+__global__ void __launch_bounds__(64) wait_selftest_kernel(volatile uint64_t* err, uint32_t limit) {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ volatile int s_abort;
+    if (threadIdx.x == 0) {
+        mi_bar_init(&bar, 1);
+        s_abort = 0;
+    }
+    __syncthreads();
+    mi_wait_scope<false>(mi_smem(&bar), 0, &s_abort, err, limit);
+}
+
 template <int BN, bool SPLIT, bool PAIR, bool CLASSES>
 constexpr int mi_kernel_bit() {
     return CLASSES ? 13 : 1 + (BN == 32 ? 0 : BN == 128 ? 4 : 8) + 2 * SPLIT + PAIR;
@@ -973,10 +986,7 @@ int fp_matmul_i8(fp_ctx* c, const int8_t* w, int64_t ldw, const float* w_scale, 
     if (((uintptr_t)w_scale | (uintptr_t)x_scale | (uintptr_t)offsets) % 4 || (uintptr_t)y % ys)
         return fp_fail(c, FP_ERR_ARG, "fp_matmul_i8: an address is not a multiple of its element size");
     if (!c) return FP_ERR_ARG;
-    if (c->mb->op_err) {
-        c->mb->op_err = 0;
-        return fp_fail(c, FP_ERR_TIMEOUT, "fp_matmul_i8: a wait of an earlier call ran out on the device; its y is not valid");
-    }
+    if (int rc = fp_op_pending(c, "fp_matmul_i8")) return rc;
     if (empty) return FP_OK;
     FpDeviceScope dev(c);
     if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_matmul_i8");
@@ -1006,4 +1016,19 @@ int fp_matmul_i8(fp_ctx* c, const int8_t* w, int64_t ldw, const float* w_scale, 
     }
     fp_toc(c, st, slot);
     return rc;
+}
+
+int fp_ops_status(fp_ctx* c) { return c ? fp_op_pending(c, "fp_ops_status") : FP_ERR_ARG; }
+
+int fp_ops_selftest(fp_ctx* c, void* stream) {
+    if (!c) return FP_ERR_ARG;
+    if (int rc = fp_op_pending(c, "fp_ops_selftest")) return rc;
+    FpDeviceScope dev(c);
+    if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_ops_selftest");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(64);
+    cfg.stream = (cudaStream_t)stream;
+    FP_CUDA(c, cudaLaunchKernelEx(&cfg, wait_selftest_kernel, (volatile uint64_t*)&c->mb_dev->op_err, 1u << 10));
+    return FP_OK;
 }

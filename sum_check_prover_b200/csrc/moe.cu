@@ -563,6 +563,7 @@ int fp_moe_sort(fp_ctx* c, const int32_t* e, int64_t n, int E, int32_t* offsets,
     if (((uintptr_t)e | (uintptr_t)offsets | (uintptr_t)pos) % 4)
         return fp_fail(c, FP_ERR_ARG, "fp_moe_sort: an address is not a multiple of its element size");
     if (!c) return FP_ERR_ARG;
+    if (int rc = fp_op_pending(c, "fp_moe_sort")) return rc;
     FpDeviceScope dev(c);
     if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_moe_sort");
     cudaStream_t st = (cudaStream_t)stream;
@@ -611,6 +612,7 @@ int fp_moe_dispatch(fp_ctx* c, const void* x, int64_t T, int64_t row_bytes, int6
     if (!empty && (!x || !pos || !rows)) return fp_fail(c, FP_ERR_ARG, "fp_moe_dispatch: null argument");
     if ((uintptr_t)pos % 4) return fp_fail(c, FP_ERR_ARG, "fp_moe_dispatch: an address is not a multiple of its element size");
     if (!c) return FP_ERR_ARG;
+    if ((rc = fp_op_pending(c, "fp_moe_dispatch"))) return rc;
     if (empty) return FP_OK;
     FpDeviceScope dev(c);
     if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_moe_dispatch");
@@ -659,6 +661,7 @@ int fp_moe_combine(fp_ctx* c, const void* rows, int rows_type, int64_t R, int64_
     if ((uintptr_t)rows % rs || ((uintptr_t)base | (uintptr_t)out) % os || ((uintptr_t)pos | (uintptr_t)weights) % 4)
         return fp_fail(c, FP_ERR_ARG, "fp_moe_combine: an address is not a multiple of its element size");
     if (!c) return FP_ERR_ARG;
+    if ((rc = fp_op_pending(c, "fp_moe_combine"))) return rc;
     if (empty) return FP_OK;
     FpDeviceScope dev(c);
     if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_moe_combine");
@@ -718,6 +721,7 @@ int fp_moe_combine_grad(fp_ctx* c, const void* dout, int out_type, int64_t ldd, 
         ((uintptr_t)pos | (uintptr_t)weights | (uintptr_t)dweights) % 4)
         return fp_fail(c, FP_ERR_ARG, "fp_moe_combine_grad: an address is not a multiple of its element size");
     if (!c) return FP_ERR_ARG;
+    if ((rc = fp_op_pending(c, "fp_moe_combine_grad"))) return rc;
     if (empty) return FP_OK;
     FpDeviceScope dev(c);
     if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_moe_combine_grad");

@@ -341,6 +341,7 @@ int fp_quantize_rows(fp_ctx* c, const void* x, int x_type, int64_t T, int64_t K,
     if ((uintptr_t)x % fp_type_size(x_type) || (uintptr_t)scale % 4 || (uintptr_t)pos % 4)
         return fp_fail(c, FP_ERR_ARG, "fp_quantize_rows: an address is not a multiple of its element size");
     if (!c) return FP_ERR_ARG;
+    if (int rc = fp_op_pending(c, "fp_quantize_rows")) return rc;
     if (empty) return FP_OK;
     FpDeviceScope dev(c);
     if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_quantize_rows");

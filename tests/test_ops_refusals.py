@@ -207,3 +207,7 @@ def test_counts_past_an_int(ctx):
     refused(lambda: ctx.moe_dispatch(T(1, 8), T(1, big + 1, dtype="int32"), T(4, 8), stream=0), "pos' choices")
     refused(lambda: ctx.matmul_i8(T(big + 1, 1, 1, dtype="int8"), T(4, 1, dtype="int8"), T(4, 1), T(big + 1, 1), T(4),
                                   offsets=T(big + 2, dtype="int32"), stream=0), "experts must be below")
+
+
+def test_status_without_a_context(fp):
+    assert fp.lib().fp_ops_status(None) == ARG and fp.lib().fp_ops_selftest(None, None) == ARG

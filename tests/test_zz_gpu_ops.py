@@ -1225,3 +1225,56 @@ def test_products_follow_other_calls(env, T, k, E, K, M):
 
     for a, b in zip(run(True), run(False)):
         assert bool(a.any()) and torch.equal(a, b)
+
+
+# ---- a bounded wait that ran out ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("way", ["binding", "methods"])
+def test_a_wait_that_ran_out_is_reported_once(env, monkeypatch, way):
+    # by whichever call comes next, which then queues nothing, or by the status; the context stays usable
+    torch, fp, _ = env
+    if way == "methods":
+        unbound(fp, monkeypatch)
+    ctx = fp.Context(0)
+    try:
+        T, k, K, M, E = 6, 2, 32, 24, 3
+        x, out = torch.randn(T, K, device="cuda"), torch.zeros(T, M, device="cuda")
+        e = torch.randint(0, E, (T, k), device="cuda", dtype=torch.int32)
+        off, pos = torch.zeros(E + 1, dtype=torch.int32, device="cuda"), torch.zeros_like(e)
+        q, s = torch.zeros(T * k, K, dtype=torch.int8, device="cuda"), torch.zeros(T * k, device="cuda")
+        rows, y = torch.zeros(T * k, K, device="cuda"), torch.zeros(T * k, M, device="cuda")
+        w, ws = torch.ones(E, M, K, dtype=torch.int8, device="cuda"), torch.ones(E, M, device="cuda")
+        dw = torch.zeros(T, k, device="cuda")
+        calls = [(off, lambda: ctx.moe_sort(e, E, off, pos)), (q, lambda: ctx.quantize_rows(x, q, s, pos=pos)),
+                 (rows, lambda: ctx.moe_dispatch(x, pos, rows)), (y, lambda: ctx.matmul_i8(w, q, y, ws, s, offsets=off)),
+                 (out, lambda: ctx.moe_combine(y, pos, out)), (dw, lambda: ctx.moe_combine_grad(out, y, pos, dweights=dw)),
+                 (None, ctx.ops_status), (None, ctx.ops_selftest)]
+        ctx.ops_status()
+        for written, call in calls:
+            before = None if written is None else written.clone()
+            ctx.ops_selftest()
+            torch.cuda.synchronize()
+            with pytest.raises(fp.FpError, match="ran out") as err:
+                call()
+            assert err.value.code == -4
+            torch.cuda.synchronize()
+            assert before is None or torch.equal(written, before)
+            ctx.ops_status()
+            if call != ctx.ops_selftest:
+                call()
+        torch.cuda.synchronize()
+        assert bool(out.any())
+        # a captured one is reported after the replay, and again after the next
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ctx.ops_selftest()
+        ctx.ops_status()
+        for _ in range(2):
+            g.replay()
+            torch.cuda.synchronize()
+            with pytest.raises(fp.FpError):
+                ctx.ops_status()
+            ctx.ops_status()
+        del g
+    finally:
+        ctx.close()
