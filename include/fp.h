@@ -812,7 +812,7 @@ int fp_moe_sort(fp_ctx* ctx, const int32_t* e, int64_t n, int E, int32_t* offset
  * Rows to their experts: rows[pos[t][j]] = x[t] for every j < k; positions outside [0, R) are passed
  * over and rows that no token goes to are left as they were. Rows are bytes of any type: row_bytes of
  * them, pitches ldx and ldr in bytes. Its gradient is fp_moe_combine without weights.
- * 0 <= T <= 2^24, k >= 1, T k < 2^31, 0 <= R < 2^31, 1 <= row_bytes <= 2^24.
+ * 0 <= T <= 2^24, 1 <= k <= 2^30, T k < 2^31, 0 <= R < 2^31, 1 <= row_bytes <= 2^24.
  */
 int fp_moe_dispatch(fp_ctx* ctx, const void* x, int64_t T, int64_t row_bytes, int64_t ldx, const int32_t* pos, int k,
                     int64_t R, void* rows, int64_t ldr, void* stream);
@@ -822,7 +822,7 @@ int fp_moe_dispatch(fp_ctx* ctx, const void* x, int64_t T, int64_t row_bytes, in
  * in fp32 in the order of j and rounded once; positions outside [0, R) add nothing.
  *  weights  nullable (all 1): T x k fp32.   base  nullable (0): T rows of M of out_type, pitch ldb, for
  *           instance a shared expert's output; base may be out.
- * 0 <= T <= 2^24, k >= 1, T k < 2^31, 0 <= R < 2^31, 1 <= M <= 2^24.
+ * 0 <= T <= 2^24, 1 <= k <= 2^30, T k < 2^31, 0 <= R < 2^31, 1 <= M <= 2^24.
  */
 int fp_moe_combine(fp_ctx* ctx, const void* rows, int rows_type, int64_t R, int64_t ldr, const int32_t* pos,
                    const float* weights, const void* base, int64_t ldb, int64_t T, int k, int64_t M, void* out,

@@ -546,11 +546,13 @@ void by_type(int type, F&& f) {
         f((__nv_bfloat16*)nullptr);
 }
 
-// positions: T x k of them, rows 0 .. R - 1
+// positions: T x k of them, rows 0 .. R - 1. The kernels step over a token's choices, several at a time, in 32 bits: up to
+// 2^30 of them, so that no step passes 2^31.
 int check_positions(fp_ctx* c, const char* what, int64_t T, int k, int64_t R) {
     if (T < 0 || T > (1ll << 24) || R < 0 || R > 0x7fffffffll)
         return fp_fail(c, FP_ERR_SHAPE, std::string(what) + ": T outside [0, 2^24] or R outside [0, 2^31)");
-    if (k < 1 || T * k > 0x7fffffffll) return fp_fail(c, FP_ERR_SHAPE, std::string(what) + ": k < 1 or T k above 2^31 - 1");
+    if (k < 1 || k > (1 << 30) || T * k > 0x7fffffffll)
+        return fp_fail(c, FP_ERR_SHAPE, std::string(what) + ": k outside [1, 2^30] or T k above 2^31 - 1");
     return FP_OK;
 }
 

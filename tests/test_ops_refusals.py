@@ -211,3 +211,12 @@ def test_counts_past_an_int(ctx):
 
 def test_status_without_a_context(fp):
     assert fp.lib().fp_ops_status(None) == ARG and fp.lib().fp_ops_selftest(None, None) == ARG
+
+
+def test_choices_past_what_the_kernels_step_over(fp):
+    # a single token with more than 2^30 choices: steps of several at a time would pass 2^31
+    L = fp.lib()
+    for k, code in (((1 << 31) - 1, SHAPE), ((1 << 30) + 1, SHAPE), (1 << 30, ARG)):  # ARG: nothing wrong but the context
+        assert L.fp_moe_dispatch(None, P, 1, 8, 8, P, k, 8, P, 8, None) == code
+        assert L.fp_moe_combine(None, P, 2, 8, 8, P, None, None, 0, 1, k, 8, P, 2, 8, None) == code
+        assert L.fp_moe_combine_grad(None, P, 2, 8, P, 2, 8, 8, P, None, 1, k, 8, P, 8, P, None) == code
