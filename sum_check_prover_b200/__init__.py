@@ -658,6 +658,11 @@ def _dtype(t) -> str:
     return got
 
 
+def _lazy(t) -> bool:
+    """Whether PyTorch has yet to conjugate or negate what lies at the tensor's address."""
+    return any(getattr(t, what, bool)() for what in ("is_conj", "is_neg"))
+
+
 def _times(shape) -> str:
     return " x ".join(map(str, shape))
 
@@ -1051,12 +1056,14 @@ class Context:
             raise ValueError(f"{what}: {name} must be {dtype}, not {_dtype(t)}")
         if t.get_device() != self.device:
             raise ValueError(f"{what}: {name} must be on cuda:{self.device}, not {t.device}")
+        if _lazy(t):
+            raise ValueError(f"{what}: {name} must be resolved first (resolve_conj, resolve_neg)")
         raise ValueError(f"{what}: {name} must be contiguous" if dense else
                          f"{what}: {name}'s rows must be contiguous and apart")
 
     def _dense(self, what: str, name: str, t, shape: tuple, dtype: str) -> int:
         """Check a contiguous tensor of one shape and type on the context's device; its address."""
-        if t.shape != shape or _dtype(t) != dtype or t.get_device() != self.device or not t.is_contiguous():
+        if t.shape != shape or _dtype(t) != dtype or t.get_device() != self.device or not t.is_contiguous() or _lazy(t):
             self._refuse(what, name, t, shape, dtype, True)
         return t.data_ptr()
 
@@ -1069,7 +1076,7 @@ class Context:
         n, m = shape
         ld, step = t.stride()
         if ((rows is not None and n != rows) or (cols is not None and m != cols) or t.get_device() != self.device
-                or (dtype is not None and _dtype(t) != dtype) or (step != 1 and m > 1) or (ld < m and n > 1)):
+                or (dtype is not None and _dtype(t) != dtype) or (step != 1 and m > 1) or (ld < m and n > 1) or _lazy(t)):
             self._refuse(what, name, t, (rows, cols), dtype, False)
         return t.data_ptr(), n, m, (ld if n > 1 else m)
 

@@ -42,11 +42,11 @@ bool call_of(PyObject* handle, PyObject* device, PyObject* stream, Call& c) {
     return number && !PyErr_Occurred();
 }
 
-// a plain tensor (no subclass, no wrapper) on the context's device
+// a plain tensor (no subclass, no wrapper, nothing still to be conjugated or negated) on the context's device
 const at::Tensor* tensor_of(PyObject* o, const Call& c, int64_t dims) {
     if (!THPVariable_CheckExact(o)) return nullptr;
     const at::Tensor& t = THPVariable_Unpack(o);
-    const bool plain = t.defined() && t.layout() == at::kStrided && t.is_cuda();
+    const bool plain = t.defined() && t.layout() == at::kStrided && t.is_cuda() && !t.is_conj() && !t.is_neg();
     return plain && t.get_device() == c.device && t.dim() == dims ? &t : nullptr;
 }
 

@@ -220,3 +220,20 @@ def test_choices_past_what_the_kernels_step_over(fp):
         assert L.fp_moe_dispatch(None, P, 1, 8, 8, P, k, 8, P, 8, None) == code
         assert L.fp_moe_combine(None, P, 2, 8, 8, P, None, None, 0, 1, k, 8, P, 2, 8, None) == code
         assert L.fp_moe_combine_grad(None, P, 2, 8, P, 2, 8, 8, P, None, 1, k, 8, P, 8, P, None) == code
+
+
+def test_values_still_to_be_conjugated_or_negated(ctx):
+    # such a view has another tensor's values at its address
+    class Conj(T):
+        def is_conj(self):
+            return True
+
+    class Neg(T):
+        def is_neg(self):
+            return True
+
+    pos = T(4, 1, dtype="int32")
+    refused(lambda: ctx.moe_dispatch(Conj(4, 8), pos, T(4, 8), stream=0), "x must be resolved")
+    refused(lambda: ctx.moe_dispatch(T(4, 8), pos, Conj(4, 8), stream=0), "rows must be resolved")
+    refused(lambda: ctx.quantize_rows(Neg(4, 8), T(4, 8, dtype="int8"), T(4), stream=0), "x must be resolved")
+    refused(lambda: ctx.quantize_rows(T(4, 8), T(4, 8, dtype="int8"), Neg(4), stream=0), "scale must be resolved")

@@ -1278,3 +1278,23 @@ def test_a_wait_that_ran_out_is_reported_once(env, monkeypatch, way):
         del g
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("way", ["binding", "methods"])
+def test_views_still_to_be_conjugated_or_negated(env, monkeypatch, way):
+    torch, fp, ctx = env
+    if way == "methods":
+        unbound(fp, monkeypatch)
+    z = torch.randn(4, 8, dtype=torch.complex64, device="cuda")
+    pos, rows = torch.arange(4, dtype=torch.int32, device="cuda")[:, None], torch.zeros_like(z)
+    neg = torch._neg_view(z.real.contiguous())
+    q, s = torch.zeros(4, 8, dtype=torch.int8, device="cuda"), torch.zeros(4, device="cuda")
+    for call in (lambda: ctx.moe_dispatch(z.conj(), pos, rows), lambda: ctx.moe_dispatch(z, pos, rows.conj()),
+                 lambda: ctx.quantize_rows(neg, q, s), lambda: ctx.quantize_rows(neg.resolve_neg(), q, torch._neg_view(s)),
+                 lambda: ctx.moe_combine(neg, pos, z.real.contiguous())):
+        with pytest.raises(ValueError, match="resolved"):
+            call()
+    ctx.moe_dispatch(z.conj().resolve_conj(), pos, rows)
+    assert torch.equal(rows, z.conj())
+    ctx.quantize_rows(neg.resolve_neg(), q, s)
+    assert np.array_equal(q.cpu().numpy(), quantized(-z.real.double().cpu().numpy())[0])
