@@ -19,6 +19,7 @@ int fp_fail(fp_ctx* c, int code, const std::string& msg) {
 }
 
 int fp_cuda_check(fp_ctx* c, cudaError_t e, const char* what) {
+    cudaGetLastError();  // reported here: not again by a later call that asks for the last error
     return fp_fail(c, FP_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
@@ -50,12 +51,9 @@ static bool profiler_injected() {
 fp_ctx* fp_ctx_create(int device) {
     fp_ctx* c = new fp_ctx();
     c->device = device;
-    if (cudaSetDevice(device) != cudaSuccess) {
-        delete c;
-        return nullptr;
-    }
     cudaDeviceProp prop;
-    if (cudaGetDeviceProperties(&prop, device) != cudaSuccess) {
+    if (cudaSetDevice(device) != cudaSuccess || cudaGetDeviceProperties(&prop, device) != cudaSuccess) {
+        cudaGetLastError();
         delete c;
         return nullptr;
     }

@@ -236,13 +236,13 @@ __global__ void __launch_bounds__(FP_ROW_THREADS)
 }
 
 template <int A>
-void launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, int64_t ldx, const int32_t* pos, int k,
+cudaError_t launch_dispatch(const fp_ctx* c, const void* x, int64_t T, int64_t bytes, int64_t ldx, const int32_t* pos, int k,
                      int64_t R, void* rows, int64_t ldr, cudaStream_t st) {
     const int nvec = (int)(bytes / A);
     constexpr int U = A == 16 ? 2 : 4;
     const FpRowGrid g = fp_row_grid(c, T, nvec, U, true);
-    fp_launch(moe_dispatch_kernel<A, U>, dim3(g.gx, g.gy), g.threads(), 0, st, (const char*)x, T, nvec, ldx, pos, k, R,
-                                                                        (char*)rows, ldr, g.tpr);
+    return fp_launch(moe_dispatch_kernel<A, U>, dim3(g.gx, g.gy), g.threads(), 0, st, (const char*)x, T, nvec, ldx, pos, k, R,
+                     (char*)rows, ldr, g.tpr);
 }
 
 // ---- combine --------------------------------------------------------------------------------
@@ -624,6 +624,7 @@ int fp_moe_dispatch(fp_ctx* c, const void* x, int64_t T, int64_t row_bytes, int6
     const int al = fp_common_align({(uint64_t)(uintptr_t)x, (uint64_t)(uintptr_t)rows, (uint64_t)ldx, (uint64_t)ldr,
                                     (uint64_t)row_bytes});
     int slot;
+    cudaError_t launched;
     fp_op_tic(c, st, K_MOE_DISPATCH, (double)row_bytes * (T + T * (double)k) + 4.0 * T * k, &slot);
     // Units of 1, 2 or 4 bytes against 16 shifted ones, us: 8192 rows of 5121 bytes 65.5 and 20.0, 20000 x 2 of 1030 24.6
     // and 22.5; 8192 x 2 of 10242 66.3 and 48.4, 4787 x 3 of 1344 10.0 and 10.6; 8192 x 2 of 16396 89.7 and 80.6, 20000 x
@@ -631,20 +632,20 @@ int fp_moe_dispatch(fp_ctx* c, const void* x, int64_t T, int64_t row_bytes, int6
     if (al <= 4 && row_bytes >= 1024 * al && T * k * row_bytes >= (1 << 21)) {
         const FpRowGrid g = fp_row_grid(c, T, row_bytes / 16, 1, true);
         const int64_t gz = std::max<int64_t>(1, std::min<int64_t>(k, 4 * (int64_t)c->num_sms / ((int64_t)g.gx * g.gy)));
-        fp_launch(moe_dispatch_any_kernel, dim3(g.gx, g.gy, (unsigned)gz), g.threads(), 0, st,
-            (const uint8_t*)x, T, row_bytes, ldx, pos, k, R, (uint8_t*)rows, ldr, g.tpr);
+        launched = fp_launch(moe_dispatch_any_kernel, dim3(g.gx, g.gy, (unsigned)gz), g.threads(), 0, st,
+                             (const uint8_t*)x, T, row_bytes, ldx, pos, k, R, (uint8_t*)rows, ldr, g.tpr);
     } else if (al >= 16)
-        launch_dispatch<16>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launched = launch_dispatch<16>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 8)
-        launch_dispatch<8>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launched = launch_dispatch<8>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 4)
-        launch_dispatch<4>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launched = launch_dispatch<4>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else if (al >= 2)
-        launch_dispatch<2>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launched = launch_dispatch<2>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     else
-        launch_dispatch<1>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
+        launched = launch_dispatch<1>(c, x, T, row_bytes, ldx, pos, k, R, rows, ldr, st);
     fp_toc(c, st, slot);
-    FP_CUDA(c, cudaGetLastError());
+    FP_CUDA(c, launched);
     return FP_OK;
 }
 
@@ -672,6 +673,7 @@ int fp_moe_combine(fp_ctx* c, const void* rows, int rows_type, int64_t R, int64_
     if (T == 1) ldo = ldb = 0;
     if (!base) ldb = 0;
     int slot;
+    cudaError_t launched = cudaSuccess;
     fp_op_tic(c, st, K_MOE_COMBINE, (double)M * (rs * (double)T * k + os * (double)T * (base ? 2 : 1)) + 8.0 * T * k, &slot);
     by_type(rows_type, [&](auto* rp) {
         using RT = std::remove_pointer_t<decltype(rp)>;
@@ -687,8 +689,8 @@ int fp_moe_combine(fp_ctx* c, const void* rows, int rows_type, int64_t R, int64_
             const int nvec = (int)(vec || odd ? M / V : M);
             auto run = [&](auto kern, int loads, int width) {
                 const FpRowGrid g = fp_row_grid(c, T, nvec, loads, true);
-                fp_launch(kern, dim3(g.gx, g.gy), g.threads(), 0, st, (const RT*)rows, R, ldr, pos, weights, (const OT*)base, ldb, T,
-                                                               k, width, (OT*)out, ldo, g.tpr);
+                launched = fp_launch(kern, dim3(g.gx, g.gy), g.threads(), 0, st, (const RT*)rows, R, ldr, pos, weights,
+                                     (const OT*)base, ldb, T, k, width, (OT*)out, ldo, g.tpr);
             };
             if constexpr (sizeof(RT) == 2) {
                 if (odd) return run(moe_combine_odd_kernel<RT, OT, V>, 1, (int)M);
@@ -702,7 +704,7 @@ int fp_moe_combine(fp_ctx* c, const void* rows, int rows_type, int64_t R, int64_
         });
     });
     fp_toc(c, st, slot);
-    FP_CUDA(c, cudaGetLastError());
+    FP_CUDA(c, launched);
     return FP_OK;
 }
 
@@ -733,6 +735,7 @@ int fp_moe_combine_grad(fp_ctx* c, const void* dout, int out_type, int64_t ldd, 
     if (T == 1) ldd = 0;
     const void* rd = dweights ? rows : nullptr;
     int slot;
+    cudaError_t launched = cudaSuccess;
     fp_op_tic(c, st, K_MOE_GRAD,
               (double)M * (os * (double)T + rs * (double)T * k * ((drows ? 1 : 0) + (dweights ? 1 : 0))) + 12.0 * T * k, &slot);
     by_type(rows_type, [&](auto* rp) {
@@ -761,14 +764,15 @@ int fp_moe_combine_grad(fp_ctx* c, const void* dout, int out_type, int64_t ldd, 
             };
             auto run = [&](auto kern, int loads) {
                 const FpRowGrid g = grid(loads, 2);
-                fp_launch(kern, dim3(g.gx, g.gy), g.threads(), 0, st, (const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k,
-                                                               nvec, (RT*)drows, lddr, dweights, g.tpr, dvec);
+                launched = fp_launch(kern, dim3(g.gx, g.gy), g.threads(), 0, st, (const OT*)dout, ldd, (const RT*)rd, R, ldr, pos,
+                                     weights, T, k, nvec, (RT*)drows, lddr, dweights, g.tpr, dvec);
             };
             if constexpr (sizeof(RT) == 2) {
                 if (odd) {
                     const FpRowGrid g = grid(1, 1);
-                    fp_launch(moe_grad_odd_kernel<RT, OT, V>, dim3(g.gx, g.gy), g.threads(), 0, st,
-                        (const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k, (int)M, (RT*)drows, lddr, dweights, g.tpr);
+                    launched = fp_launch(moe_grad_odd_kernel<RT, OT, V>, dim3(g.gx, g.gy), g.threads(), 0, st,
+                                         (const OT*)dout, ldd, (const RT*)rd, R, ldr, pos, weights, T, k, (int)M, (RT*)drows, lddr,
+                                         dweights, g.tpr);
                     return;
                 }
             }
@@ -779,6 +783,6 @@ int fp_moe_combine_grad(fp_ctx* c, const void* dout, int out_type, int64_t ldd, 
         });
     });
     fp_toc(c, st, slot);
-    FP_CUDA(c, cudaGetLastError());
+    FP_CUDA(c, launched);
     return FP_OK;
 }

@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(256, 4)
 }
 
 template <typename T>
-void launch_quant(const fp_ctx* c, const void* x, int64_t T_, int64_t K, int64_t ldx, const int32_t* pos, int k,
+cudaError_t launch_quant(const fp_ctx* c, const void* x, int64_t T_, int64_t K, int64_t ldx, const int32_t* pos, int k,
                   int64_t R, int8_t* q, int64_t ldq, float* scale, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
     const bool plain = K % V == 0 && fp_common_align({(uint64_t)(uintptr_t)q, (uint64_t)ldq}) >= V &&
@@ -315,14 +315,11 @@ void launch_quant(const fp_ctx* c, const void* x, int64_t T_, int64_t K, int64_t
     const int threads = std::max(128 / tpr, 1) * tpr;
     const unsigned grid = (unsigned)((T_ + threads / tpr - 1) / (threads / tpr));
     auto run = [&](auto kern, int smem) {
-        fp_launch(kern, grid, threads, smem, st, (const T*)x, T_, (int)K, ldx, pos, k, R, q, ldq, scale, tpr);
+        return fp_launch(kern, grid, threads, smem, st, (const T*)x, T_, (int)K, ldx, pos, k, R, q, ldq, scale, tpr);
     };
-    if (plain)
-        run(quant_rows_kernel<T, V, QR_LOADS>, 0);
-    else if (single)
-        run(quant_rows_kernel<T, 1, 2 * QR_LOADS>, 0);
-    else
-        run(quant_odd_rows_kernel<T, V>, threads / tpr * (tpr * QR_LOADS * V + 16));
+    if (plain) return run(quant_rows_kernel<T, V, QR_LOADS>, 0);
+    if (single) return run(quant_rows_kernel<T, 1, 2 * QR_LOADS>, 0);
+    return run(quant_odd_rows_kernel<T, V>, threads / tpr * (tpr * QR_LOADS * V + 16));
 }
 
 }  // namespace
@@ -350,13 +347,11 @@ int fp_quantize_rows(fp_ctx* c, const void* x, int x_type, int64_t T, int64_t K,
     if (R == 1) ldq = 16;
     int slot;
     fp_op_tic(c, st, K_QUANT_ROWS, (double)T * K * fp_type_size(x_type) + (double)(pos ? T * k : T) * (K + 4), &slot);
-    if (x_type == FP_F32)
-        launch_quant<float>(c, x, T, K, ldx, pos, k, R, q, ldq, scale, st);
-    else if (x_type == FP_F16)
-        launch_quant<__half>(c, x, T, K, ldx, pos, k, R, q, ldq, scale, st);
-    else
-        launch_quant<__nv_bfloat16>(c, x, T, K, ldx, pos, k, R, q, ldq, scale, st);
+    const auto launch = x_type == FP_F32   ? launch_quant<float>
+                        : x_type == FP_F16 ? launch_quant<__half>
+                                           : launch_quant<__nv_bfloat16>;
+    const cudaError_t rc = launch(c, x, T, K, ldx, pos, k, R, q, ldq, scale, st);
     fp_toc(c, st, slot);
-    FP_CUDA(c, cudaGetLastError());
+    FP_CUDA(c, rc);
     return FP_OK;
 }

@@ -1298,3 +1298,18 @@ def test_views_still_to_be_conjugated_or_negated(env, monkeypatch, way):
     assert torch.equal(rows, z.conj())
     ctx.quantize_rows(neg.resolve_neg(), q, s)
     assert np.array_equal(q.cpu().numpy(), quantized(-z.real.double().cpu().numpy())[0])
+
+
+def test_earlier_errors_are_not_the_operators(env):
+    # a context for a device that is not there leaves an error behind; calls that are queued do not report it
+    torch, fp, ctx = env
+    x, pos = torch.randn(5, 32, device="cuda"), torch.arange(5, dtype=torch.int32, device="cuda")[:, None]
+    q, s, rows, out = torch.zeros(5, 32, dtype=torch.int8, device="cuda"), torch.zeros(5, device="cuda"), torch.zeros_like(x), torch.zeros_like(x)
+    dw, w, y = torch.zeros(5, 1, device="cuda"), torch.ones(7, 32, dtype=torch.int8, device="cuda"), torch.zeros(5, 7, device="cuda")
+    for call in (lambda: ctx.quantize_rows(x, q, s), lambda: ctx.moe_dispatch(x, pos, rows), lambda: ctx.moe_combine(rows, pos, out),
+                 lambda: ctx.moe_combine_grad(x, rows, pos, dweights=dw), lambda: ctx.matmul_i8(w, q, y, torch.ones(7, device="cuda"), s),
+                 lambda: ctx.moe_sort(pos, 4, pos.new_zeros(5), pos.new_zeros(5, 1))):
+        with pytest.raises(fp.FpError):
+            fp.Context(1000)
+        call()
+    assert torch.equal(rows, x) and torch.equal(out, x)
