@@ -8,6 +8,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -63,11 +64,13 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> Path | None:
-    """Compile csrc/binding.cpp for this interpreter and its PyTorch; None where either lacks what that takes (the
-    operators' methods then do without it)."""
+    """Compile csrc/binding.cpp for this interpreter and its PyTorch; None where either lacks what that takes or the
+    compiler fails (with a warning: the library is whole, and the operators' methods then do without it)."""
     spec, python = importlib.util.find_spec("torch"), Path(sysconfig.get_paths()["include"])
     root = Path(spec.origin).resolve().parent if spec and spec.origin else None
-    if root is None or not (root / "lib" / "libc10_cuda.so").exists() or not (python / "Python.h").exists():
+    if root is None or not all(p.exists() for p in (
+            root / "lib" / "libc10_cuda.so", root / "include" / "torch" / "csrc" / "autograd" / "python_variable.h", python / "Python.h")):
+        BINDING.unlink(missing_ok=True)
         return None
     src = CSRC / "binding.cpp"
     newest = max(p.stat().st_mtime for p in (src, INCLUDE / "fp.h", Path(__file__), root / "version.py"))
@@ -80,9 +83,16 @@ def build_binding(force: bool = False, verbose: bool = False) -> Path | None:
            "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed:\n{r.stderr}{r.stdout}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.stderr + r.stdout if r.returncode else ""
+    except OSError as e:
+        failed = str(e)
+    if failed or not tmp.exists():
+        for p in (tmp, BINDING):  # (an older one may not know the library)
+            p.unlink(missing_ok=True)
+        warnings.warn(f"{BINDING.name} was not built, the layer operators' calls go without it; {cmd[0]}:\n{failed}")
+        return None
     os.replace(tmp, BINDING)
     return BINDING
 
