@@ -65,11 +65,14 @@ class _Unbound:
 
 def _load_binding():
     global _bound
+    _bound = _Unbound
     try:
-        import torch  # noqa: F401  (the libraries that it links against)
-        from . import _binding as _bound
+        import torch  # (the libraries that it links against)
+        from . import _binding
+        if _binding.torch == str(torch.__version__):  # (another's tensors may lie differently in memory)
+            _bound = _binding
     except ImportError:
-        _bound = _Unbound
+        pass
     return _bound
 
 

@@ -1,10 +1,11 @@
-"""Build libfp.so in-tree with nvcc for sm_100a (cross-compiles without a GPU), and beside it _binding.so, the
+"""Build libfp.so in-tree with nvcc for sm_100a (cross-compiles without a GPU), and beside it the module _binding, the
 layer operators' short way from PyTorch's tensors into it."""
 
 from __future__ import annotations
 
 import importlib.util
 import os
+import runpy
 import subprocess
 import sys
 import sysconfig
@@ -17,7 +18,8 @@ CSRC = HERE / "csrc"
 INCLUDE = HERE.parent / "include"
 OBJ = HERE / "_build"
 LIB = HERE / "libfp.so"
-BINDING = HERE / "_binding.so"
+# (named for the interpreter that it is built for, so that another one does not import it)
+BINDING = HERE / ("_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -69,15 +71,21 @@ def build_binding(force: bool = False, verbose: bool = False) -> Path | None:
     spec, python = importlib.util.find_spec("torch"), Path(sysconfig.get_paths()["include"])
     root = Path(spec.origin).resolve().parent if spec and spec.origin else None
     if root is None or not all(p.exists() for p in (
-            root / "lib" / "libc10_cuda.so", root / "include" / "torch" / "csrc" / "autograd" / "python_variable.h", python / "Python.h")):
+            root / "lib" / "libc10_cuda.so", root / "include" / "torch" / "csrc" / "autograd" / "python_variable.h", root / "version.py",
+            python / "Python.h")):
         BINDING.unlink(missing_ok=True)
         return None
+    (HERE / "_binding.so").unlink(missing_ok=True)  # (an earlier build's name, which every interpreter would import)
     src = CSRC / "binding.cpp"
-    newest = max(p.stat().st_mtime for p in (src, INCLUDE / "fp.h", Path(__file__), root / "version.py"))
-    if not force and BINDING.exists() and BINDING.stat().st_mtime >= newest:
+    newest = max(p.stat().st_mtime for p in (src, INCLUDE / "fp.h", Path(__file__)))
+    version = str(runpy.run_path(str(root / "version.py"))["__version__"])
+    OBJ.mkdir(exist_ok=True)
+    built_for = OBJ / (BINDING.name + ".torch")  # the PyTorch that the module there was compiled against
+    if (not force and BINDING.exists() and BINDING.stat().st_mtime >= newest and built_for.exists()
+            and built_for.read_text() == version):
         return BINDING
     tmp = BINDING.with_suffix(f".so.{os.getpid()}")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{root / 'include'}",
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f'-DFP_TORCH="{version}"', f"-I{root / 'include'}",
            f"-I{python}", f"-I{Path(NVCC).resolve().parents[1] / 'include'}", str(src), "-o", str(tmp),
            f"-L{root / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-L{HERE}", "-l:libfp.so",
            "-Wl,-rpath,$ORIGIN"]
@@ -89,11 +97,12 @@ def build_binding(force: bool = False, verbose: bool = False) -> Path | None:
     except OSError as e:
         failed = str(e)
     if failed or not tmp.exists():
-        for p in (tmp, BINDING):  # (an older one may not know the library)
+        for p in (tmp, BINDING, built_for):  # (an older one may not know the library)
             p.unlink(missing_ok=True)
         warnings.warn(f"{BINDING.name} was not built, the layer operators' calls go without it; {cmd[0]}:\n{failed}")
         return None
     os.replace(tmp, BINDING)
+    built_for.write_text(version)
     return BINDING
 
 

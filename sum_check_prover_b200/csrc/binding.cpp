@@ -237,4 +237,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&kModule); }
+// torch: the version of PyTorch that this was compiled against, whose tensors' layout it relies on
+PyMODINIT_FUNC PyInit__binding() {
+    PyObject* m = PyModule_Create(&kModule);
+    if (m && PyModule_AddStringConstant(m, "torch", FP_TORCH) != 0) Py_CLEAR(m);
+    return m;
+}
