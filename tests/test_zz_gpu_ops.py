@@ -1313,3 +1313,31 @@ def test_earlier_errors_are_not_the_operators(env):
             fp.Context(1000)
         call()
     assert torch.equal(rows, x) and torch.equal(out, x)
+
+
+@pytest.mark.parametrize("K", [64, 77])
+def test_matmul_offsets_past_the_rows(env, K):
+    # every offset counts as the largest up to it, inside [0, N]; nothing behind the last row is written
+    torch, fp, ctx = env
+    for off, ends in (([-5, 3, 2, 30, 2 ** 31 - 1], [0, 3, 3, 20, 20]), ([-2 ** 31, -1, 0, 20, 21], [0, 0, 0, 20, 20]),
+                      ([2, 5, 5, 9, 99], [2, 5, 5, 9, 20]), ([21, 25, 0, 7, 20], [20, 20, 20, 20, 20])):
+        w, x, ws, xs, whole, yb = product_case(torch, 24, 40, K, 4, "float32", 3, pady=3)
+        y = whole[:20]
+        whole.fill_(7)
+        before = yb.clone()
+        ctx.matmul_i8(w, x[:20], y, ws, xs[:20], offsets=torch.tensor(off, dtype=torch.int32, device="cuda"))
+        check_product(torch, w, x[:20], ws, xs[:20], y, ends)
+        assert bool((y[:ends[0]] == 7).all()) and bool((y[ends[-1]:] == 7).all())
+        untouched(torch, y, yb, before)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,M,K", [(96, 6000, 4096), (128, 4096, 8192), (200, 2900, 2048), (127, 6001, 1665)])
+def test_matmul_split_sums_of_many_tokens(env, dtype, N, M, K):
+    # tiles of 128 tokens with K split among the blocks of a cluster
+    torch, fp, ctx = env
+    w, x, ws, xs, y, yb = product_case(torch, N, M, K, 0, dtype, N + M, padx=16, pady=1)
+    before = yb.clone()
+    ctx.matmul_i8(w, x, y, ws, xs)
+    check_product(torch, w, x, ws, xs, y)
+    untouched(torch, y, yb, before)
