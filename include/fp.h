@@ -792,8 +792,8 @@ int fp_quantize_rows(fp_ctx* ctx, const void* x, int x_type, int64_t T, int64_t 
  * 1 <= M <= 2^24, 0 <= N <= 2^24, 1 <= K < 2^17 (exact int32 sums), 1 <= E <= 4096, E M < 2^31 - 255.
  * Fastest when w, x, ldw and ldx are multiples of 16. An operand whose address or pitch is not is first
  * copied (of weights the experts that have rows; none where few tokens meet them) to rows that are, in
- * stream-ordered memory of the context, which keeps it for later calls (FP_ERR_OOM if there is none);
- * inside a graph it is the graph's. The kernel's waits are bounded: should one run
+ * stream-ordered memory of the context, which keeps the most that calls had at once for later ones, until
+ * fp_ops_trim or fp_ctx_destroy (FP_ERR_OOM if there is none); inside a graph it is the graph's. The kernel's waits are bounded: should one run
  * out, the earlier y is not valid, and fp_ops_status or the next call of an operator says so.
  */
 int fp_matmul_i8(fp_ctx* ctx, const int8_t* w, int64_t ldw, const float* w_scale, int E, int64_t M, int64_t K,
@@ -845,6 +845,12 @@ int fp_moe_combine_grad(fp_ctx* ctx, const void* dout, int out_type, int64_t ldd
  * of a program or after a graph's replay, for which no later call would say so.
  */
 int fp_ops_status(fp_ctx* ctx);
+
+/*
+ * Give back the device memory that fp_matmul_i8 keeps for operands with odd pitches. What queued calls still use
+ * stays: call it when the stream has been synchronised. Later calls take memory again.
+ */
+int fp_ops_trim(fp_ctx* ctx);
 
 /*
  * Self-test of those waits: queues a kernel that waits a short time for a barrier that nothing arrives at, gives up

@@ -145,6 +145,7 @@ def lib():
     L.fp_moe_combine.argtypes = [vp, vp, i32, i64, i64, vp, vp, vp, i64, i64, i32, i64, vp, i32, i64, vp]
     L.fp_moe_combine_grad.argtypes = [vp, vp, i32, i64, vp, i32, i64, i64, vp, vp, i64, i32, i64, vp, i64, vp, vp]
     L.fp_ops_status.argtypes = [vp]
+    L.fp_ops_trim.argtypes = [vp]
     L.fp_ops_selftest.argtypes = [vp, vp]
     L.fp_ctx_set_profiling.argtypes = [vp, i32]
     L.fp_session_selftest.argtypes = [vp, vp]
@@ -1223,6 +1224,11 @@ class Context:
         earlier matmul_i8's y is not valid. The next operator raises it too; this is for a program's last one and for
         graphs' replays. It waits for nothing: synchronise the stream first."""
         self._check(self._L.fp_ops_status(self.h), "fp_ops_status")
+
+    def ops_trim(self) -> None:
+        """Give back the device memory that matmul_i8 keeps for operands with odd pitches (a copy of them). What queued
+        calls still use stays: synchronise the stream first."""
+        self._check(self._L.fp_ops_trim(self.h), "fp_ops_trim")
 
     def ops_selftest(self, stream=None) -> None:
         """Queue a kernel whose bounded wait runs out, for ops_status or the next operator to report."""

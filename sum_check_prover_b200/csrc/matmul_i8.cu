@@ -1020,6 +1020,14 @@ int fp_matmul_i8(fp_ctx* c, const int8_t* w, int64_t ldw, const float* w_scale, 
 
 int fp_ops_status(fp_ctx* c) { return c ? fp_op_pending(c, "fp_ops_status") : FP_ERR_ARG; }
 
+int fp_ops_trim(fp_ctx* c) {
+    if (!c) return FP_ERR_ARG;
+    FpDeviceScope dev(c);
+    if (dev.err != cudaSuccess) return fp_cuda_check(c, dev.err, "fp_ops_trim");
+    if (c->pool) FP_CUDA(c, cudaMemPoolTrimTo(c->pool, 0));
+    return FP_OK;
+}
+
 int fp_ops_selftest(fp_ctx* c, void* stream) {
     if (!c) return FP_ERR_ARG;
     if (int rc = fp_op_pending(c, "fp_ops_selftest")) return rc;

@@ -237,3 +237,7 @@ def test_values_still_to_be_conjugated_or_negated(ctx):
     refused(lambda: ctx.moe_dispatch(T(4, 8), pos, Conj(4, 8), stream=0), "rows must be resolved")
     refused(lambda: ctx.quantize_rows(Neg(4, 8), T(4, 8, dtype="int8"), T(4), stream=0), "x must be resolved")
     refused(lambda: ctx.quantize_rows(T(4, 8), T(4, 8, dtype="int8"), Neg(4), stream=0), "scale must be resolved")
+
+
+def test_trim_without_a_context(fp):
+    assert fp.lib().fp_ops_trim(None) == ARG
