@@ -1373,3 +1373,55 @@ def test_memory_of_odd_pitches_is_given_back(env):
         check_product(torch, w[:, :300], x, ws[:, :300], xs, y[:, :300], ends)
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_joined_streams(env, captured):
+    # a base made on a second stream, waited for between two calls of the first: neither starts before what it waits for
+    torch, fp, ctx = env
+    T, k, E, K, M = 700, 2, 8, 512, 4096
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, e = torch.randn(T, K, generator=g, device="cuda"), torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.randint(-128, 128, (E, M, K), generator=g, device="cuda", dtype=torch.int8)
+    ws, wt = torch.rand(E, M, generator=g, device="cuda") * 1e-3, torch.rand(T, k, generator=g, device="cuda")
+    a, b = (torch.randn(M, M, generator=g, device="cuda") for _ in range(2))
+    off, pos = torch.zeros(E + 1, dtype=torch.int32, device="cuda"), torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    q, s, y = torch.zeros(T * k, K, dtype=torch.int8, device="cuda"), torch.zeros(T * k, device="cuda"), torch.zeros(T * k, M, device="cuda")
+    base, out, back = torch.zeros(T, M, device="cuda"), torch.zeros(T, M, device="cuda"), torch.zeros(T, M, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work(together):
+        other = side if together else main
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            torch.mm(a[:T], b, out=base)  # takes longer than what the first stream has meanwhile
+            base.add_(1.0)
+        with torch.cuda.stream(main):
+            ctx.moe_sort(e, E, off, pos)
+            ctx.quantize_rows(x, q, s, pos=pos)
+            ctx.matmul_i8(w, q, y, ws, s, offsets=off)
+            main.wait_stream(other)
+            ctx.moe_combine(y, pos, out, weights=wt, base=base)
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            ctx.moe_combine(y, pos, back, base=out)
+            base.zero_()
+        main.wait_stream(other)
+        with torch.cuda.stream(main):
+            ctx.moe_sort(e, E, off, pos)
+
+    work(False)
+    torch.cuda.synchronize()
+    want, wanted = out.clone(), back.clone()
+    run = lambda: work(True)  # noqa: E731
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            work(True)
+        run = graph.replay
+    for _ in range(5):
+        y.zero_(), out.zero_(), back.zero_(), pos.zero_(), off.zero_()
+        torch.cuda.synchronize()
+        run()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(back, wanted)
