@@ -771,7 +771,8 @@ enum { FP_F32 = 0, FP_F16 = 1, FP_BF16 = 2 }; /* types of real values */
  * result is what fp_matmul_i8 and an fp_site's xt take.
  *  x      T rows of K values of x_type, pitch ldx.
  *  pos    nullable. Null: token t's row is row t of q and scale (R >= T). Else T x k int32: token t
- *         is written to rows pos[t][j] for every j < k; positions outside [0, R) are passed over.
+ *         is written to rows pos[t][j] for every j < k; positions outside [0, R) are passed over, those
+ *         inside are each a row's only one, as fp_moe_sort's are (of several, either may be what remains).
  *  q      R rows of K, pitch ldq. scale: R. Rows that no token goes to are left as they were.
  * 0 <= T <= 2^24, 1 <= K <= 2^20, 0 <= R < 2^31, k >= 1 and T k < 2^31 with pos.
  */
@@ -780,8 +781,9 @@ int fp_quantize_rows(fp_ctx* ctx, const void* x, int x_type, int64_t T, int64_t 
 
 /*
  * Matrix product in 8-bit integers with a scale for each token and each output channel, dense or
- * grouped by expert: y[n][m] = x_scale[n] w_scale[e][m] sum_k w[e][m][k] x[n][k]. The sum is exact;
- * it is multiplied by the token's scale, then the channel's, in fp32 and rounded to y_type.
+ * grouped by expert: y[n][m] = x_scale[n] w_scale[e][m] sum_k w[e][m][k] x[n][k]. The sum is exact in
+ * int32; it is rounded to fp32 (from 2^24 on), multiplied by the token's scale, then the channel's, in
+ * fp32 and rounded to y_type.
  *  w        E x M rows of K int8, pitch ldw; w_scale: E x M.
  *  x        N rows of K int8, pitch ldx; x_scale: N.
  *  offsets  nullable when E = 1. E + 1 int32 as fp_moe_sort writes them: expert e has the rows
@@ -810,7 +812,8 @@ int fp_moe_sort(fp_ctx* ctx, const int32_t* e, int64_t n, int E, int32_t* offset
 
 /*
  * Rows to their experts: rows[pos[t][j]] = x[t] for every j < k; positions outside [0, R) are passed
- * over and rows that no token goes to are left as they were. Rows are bytes of any type: row_bytes of
+ * over, those inside are each a row's only one (of several, either may be what remains), and rows that no
+ * token goes to are left as they were. Rows are bytes of any type: row_bytes of
  * them, pitches ldx and ldr in bytes. Its gradient is fp_moe_combine without weights.
  * 0 <= T <= 2^24, 1 <= k <= 2^30, T k < 2^31, 0 <= R < 2^31, 1 <= row_bytes <= 2^24.
  */
@@ -831,8 +834,9 @@ int fp_moe_combine(fp_ctx* ctx, const void* rows, int rows_type, int64_t R, int6
 /*
  * Gradients of fp_moe_combine from dout (T rows of M of out_type, pitch ldd; also the gradient of
  * base): drows[pos[t][j]] = weights[t][j] dout[t] and dweights[t][j] = sum_m dout[t][m]
- * rows[pos[t][j]][m], fp32 sums in a fixed order; positions outside [0, R) have dweights 0. Rows of
- * drows that no choice has are left as they were. drows (R rows of M of rows_type, pitch lddr) or
+ * rows[pos[t][j]][m], fp32 sums in a fixed order; positions outside [0, R) have dweights 0. Where drows is
+ * asked for, positions inside are each a row's only one: gradients of a row that several choices share are
+ * not summed (either may be what remains). Rows of drows that no choice has are left as they were. drows (R rows of M of rows_type, pitch lddr) or
  * dweights (T x k fp32) may be null; rows is not read without dweights. Sizes as fp_moe_combine.
  */
 int fp_moe_combine_grad(fp_ctx* ctx, const void* dout, int out_type, int64_t ldd, const void* rows, int rows_type,

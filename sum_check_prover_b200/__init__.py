@@ -1107,7 +1107,8 @@ class Context:
     def quantize_rows(self, x, q, scale, pos=None, stream=None) -> None:
         """int8 rows with one scale a token: scale = max |x| / 127, q the nearest integers to x / scale.
         x: T x K float32, float16 or bfloat16; q: R x K int8; scale: R float32. pos (T x k int32, from
-        moe_sort): token t goes to the rows pos[t], else to row t. Rows without a token are left."""
+        moe_sort): token t goes to the rows pos[t], each a row's only one, else to row t. Rows without a token
+        are left."""
         rc = (_bound or _load_binding()).quantize_rows(self.h, self.device, x, q, scale, pos, stream)
         if rc is None:
             what = "quantize_rows"
@@ -1167,9 +1168,9 @@ class Context:
             self._check(rc, "fp_moe_sort")
 
     def moe_dispatch(self, x, pos, rows, stream=None) -> None:
-        """rows[pos[t][j]] = x[t]. x: T x K of any type; pos: T x k int32; rows: R x K of x's type. The
-        experts' inputs of prove_dispatch, for any k. Rows without a token are left. Its gradient is
-        moe_combine without weights."""
+        """rows[pos[t][j]] = x[t]. x: T x K of any type; pos: T x k int32, each a row's only one; rows: R x K of
+        x's type. The experts' inputs of prove_dispatch, for any k. Rows without a token are left. Its gradient
+        is moe_combine without weights."""
         rc = (_bound or _load_binding()).moe_dispatch(self.h, self.device, x, pos, rows, stream)
         if rc is None:
             what = "moe_dispatch"
@@ -1202,7 +1203,8 @@ class Context:
     def moe_combine_grad(self, dout, rows, pos, weights=None, drows=None, dweights=None, stream=None) -> None:
         """Gradients of moe_combine: drows[pos[t][j]] = weights[t][j] dout[t] (rows' type) and
         dweights[t][j] = <dout[t], rows[pos[t][j]]> (T x k float32), either of them None when it is not
-        wanted. dout: T x M (base's gradient as it is). Rows of drows without a choice are left."""
+        wanted. dout: T x M (base's gradient as it is). For drows each position is a row's only one: gradients of
+        shared rows are not summed. Rows of drows without a choice are left."""
         rc = (_bound or _load_binding()).moe_combine_grad(self.h, self.device, dout, rows, pos, weights, drows,
                                                                 dweights, stream)
         if rc is None:
