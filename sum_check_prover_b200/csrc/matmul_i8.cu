@@ -1,7 +1,7 @@
 // fp_matmul_i8: y[n][m] = x_scale[n] w_scale[e][m] sum_k w[e][m][k] x[n][k], e the expert of row n.
 //
-// The sum is exact in int32 (K <= 2^17 - 1 keeps 2^14 K below 2^31); the three factors are multiplied in
-// fp32 in the order sum, token scale, channel scale, and rounded to y's type.
+// The sum is exact in int32 (K <= 2^17 - 1 keeps 2^14 K below 2^31); it is rounded to fp32, where it has more than 24
+// bits, and multiplied there by the token's scale, then by the channel's, and the result rounded to y's type.
 //
 // One kernel on the 5th-generation tensor cores (kind::i8, accumulators in tensor memory). A tile is 128
 // channels of one expert (the MMA's M, tensor-memory lanes) by up to BN of its tokens (the MMA's N, set
@@ -25,14 +25,19 @@
 // The cluster's barrier is awaited only by the warps that write to the others, and no block waits for another to leave
 // (4384 x 1600, 16 tokens: 6.5 us, with both waits 7.2).
 //
-// What bounds it, and what it takes (B200, repeated calls on changing inputs):
-//   many tokens    the tensor cores: 4096 x 14336 x 4096 157-161 us, 3.0 PTOP/s, 0.9 of twice the measured bf16
-//                  rate, tensor pipe 85% active. One block a tile of 128 x 256 took 187 us: its operands came to
-//                  1.5 times the L2 traffic, 15 TB/s.
-//   few a group    HBM: 128 experts of 8192 x 5120, 8192 tokens, 833 us, 6.6 TB/s; 64 tokens 276 us, 6.9.
-//   one weight     the way in and out: 5120 x 16384 for one token takes 19 us, 13 of them its 84 MB at the copy's
+// What bounds it, and what it takes (one B200, inputs that change from pass to pass):
+//   many tokens    the tensor cores, and over seconds the board's power: 4096 x 14336 x 4096 takes 160 us in a burst of
+//                  5 ms, 3.0 POP/s, the tensor pipe active 92% of the SMs' cycles at 1.56 GHz (under the profiler); calls
+//                  one after the other for 2 s take 182 us each at 1.29 of 1.965 GHz, with the power cap the only reason.
+//                  A library's int8 product of these sizes, without scales, takes 155-158 us in a burst and 180-182 over
+//                  2 s. One block a tile of 128 x 256 took 187 us in the same replays as the pairs' 157: its operands come
+//                  to 1.5 times the bytes from L2, of which the pairs take 12 TB/s.
+//   few a group    HBM: 128 experts of 8192 x 5120 over 8192 tokens 850-940 us, 5.9-6.5 TB/s; 64 tokens 280-306.
+//   one weight     the way in and out: 5120 x 16384 for one token takes 18.7 us, 13 of them its 84 MB at the copy's
 //                  rate; about 4 us are launch, first loads and epilogue, and 120 of 148 SMs have a part.
-//   small K        the epilogue: 802 x 12944 x 128 15.7 us, 21 MB of y.
+//   small K        the epilogue: 802 x 12944 x 128 15.9 us, 21 MB of y.
+// (The ranges are calls and bursts on several boards; the last two are calls, in a graph's replays 18.4 and 15.4 us. The
+// figures beside the rules below are of graph replays, both sides in turn.)
 // The issuing warps run their loops as whole warps with one elected lane: run by a lane alone the same loops took
 // 380 ns a k-tile, more than the loads (29 us for the single token).
 //
@@ -484,7 +489,8 @@ __global__ void __launch_bounds__(MI_THREADS, 1)
                 for (uint32_t i = issued > (uint32_t)S ? issued - S : 0; i < issued; i++)
                     mi_drain(full0 + 8 * (i % S), (i / S) & 1u);
             } else {
-                // (the other block's part may be missing, so that the phases never complete: time has to do)
+                // (the other block's part may be missing, so that the phases never complete: 64 ms have to do, of which
+                // the copies, on their way when the wait ran out, need a few microseconds)
                 for (int i = 0; i < 64; i++) __nanosleep(1000000);
             }
         }

@@ -212,8 +212,9 @@ __global__ void __launch_bounds__(256, 4)
 // The same for any K, addresses and pitches. The integers of tpr QR_LOADS vectors at a time go through
 // shared memory, from where each copy of the row takes 16 bytes at a time for the multiples of 16 of its addresses,
 // shifted, and the bytes before and behind them one by one. 8192 x 4099 bf16 into experts' rows, 101 MB, takes 40 us (61
-// by single values), 2.5 TB/s: about 150 instructions for 8 values (shifts, quotients, the reduction's share) and the
-// waits between the passes bound it.
+// by single values), 2.5 TB/s: about 150 instructions for 8 values (shifts, quotients, the reduction's share), the
+// waits between the passes, and spills bound it (60 bytes of a thread for bf16, 80 fp32, 136 f16, at the 64 registers
+// that four blocks of 256 threads leave it).
 template <typename T, int V>
 __global__ void __launch_bounds__(256, 4)
     quant_odd_rows_kernel(const T* __restrict__ x, int64_t rows, int K, int64_t ldx, const int32_t* __restrict__ pos,
